@@ -9,6 +9,8 @@
  *   tps_gather_rows -> the active tokens' rows (input of the QKV projection)
  *   kv_sync       -> fresh K/V rows into the layer cache (+ noise-aware re-noise)
  *   kv_rerotate   -> cached keys of pruned tokens turned to their own RoPE position
+ *   rope_rows     -> fresh Q (and K) rows turned to their token's position, or back
+ *   kv_sync_q8, pruned_attn_q8 -> the same cache and attention with 8-bit K/V
  *   pruned_attn   -> active queries attend all N cached keys (optional key-block mask)
  *   scatter_out   -> active outputs written back over the cached outputs
  *
@@ -272,6 +274,66 @@ typedef struct tps_rope {
 TPS_API int kv_rerotate(const tps_bf16* k_cache, const int32_t* idx, const int32_t* count, int64_t cap,
                         int64_t N, int H, int d, const tps_rope* rope, tps_bf16* k_eff, tps_stream stream);
 
+/* ---- rotary positions on the latent grid ([TR] Metodologia 1; [LIPAR] 2.C) ----
+ * A head's d channels are the contiguous groups [t | x | y] of dims[0], dims[1],
+ * dims[2] channels (each even, summing to d); the adjacent channels
+ * (o_a + 2j, o_a + 2j + 1) of group a are pair j, as in kv_rerotate. Token
+ * n = (f*Hs + y)*Ws + x stands at (f, x, y); pair j of group a turns by
+ *   phi = (origin[a] + position) * base^(-2j / dims[a]).
+ * The (cos, sin) of every position and pair come from a table that the caller
+ * builds once and keeps: axes t, x, y one after the other, entry (position,
+ * pair) of axis a at position * dims[a]/2 + pair.
+ * tps_rope_table fills it on the HOST (2 * sum_a size[a] * dims[a]/2 floats, cos
+ * and sin in double precision, rounded once); the caller copies it to the
+ * device. All four pointers are HOST. size[a] in [1, 2^24], |origin[a]| <= 2^24;
+ * base finite and > 0. */
+TPS_API int tps_rope_table(float* table, const int32_t* dims, const int32_t* size, const int32_t* origin, float base);
+
+typedef struct tps_rope_grid {
+  int32_t      dims[3];  /* channels of the t, x and y groups                 */
+  int32_t      size[3];  /* positions of the t, x and y axes: F, Ws, Hs       */
+  const float* table;    /* DEVICE, 16-byte aligned, from tps_rope_table      */
+} tps_rope_grid;
+
+/* Rows turned to their token's position, or back: for j < min(*count, cap),
+ *   dst[j] = R(token idx[j]) src[j]       (inverse = 0)
+ *   dst[j] = R(token idx[j])^T src[j]     (inverse = 1: the gradient of the turn)
+ * per head, fp32 from the table's entries, rounded once to bf16. src, dst
+ * [cap, H, d] bf16, dst may be src. src2 / dst2: NULL, or a second pair of tensors
+ * turned by the same launch (Q and K). idx NULL: row j is token j (cap <= N);
+ * count may then be NULL too (cap rows). Rows j >= min(*count, cap) are left as
+ * they were, and so are rows whose index lies outside [0, N) (TPS_ERR_BOUNDS at
+ * tps_check). idx needs no order here. rope is a HOST pointer; its grid must
+ * hold N tokens. d in {64, 128}; H*d <= 16384; N, cap < 2^31. */
+TPS_API int rope_rows(tps_bf16* dst, const tps_bf16* src, tps_bf16* dst2, const tps_bf16* src2, const int32_t* idx,
+                      const int32_t* count, int64_t cap, int64_t N, int H, int d, const tps_rope_grid* rope,
+                      int inverse, tps_stream stream);
+
+/* ---- 8-bit cache: update ([HSA] 2.2 (2); [TR] Metodologia 1) -------------------
+ * kv_sync for a cache held in 8 bits. k_cache, v_cache [N, H, d] hold e4m3 codes (4
+ * exponent and 3 mantissa bits, largest 448, codes 0x7F / 0xFF are NaN);
+ * k_scale, v_scale float32 [nb, H], nb = ceil(N / 128): the value of a code of token
+ * n, head h is code * scale[n / 128][h]. A cache of zero codes and zero scales is
+ * empty. For every block of 128 tokens with an active token j < min(*count, cap):
+ *   - x = k_fresh[j] turned to the position of token idx[j] as by rope_rows (fp32,
+ *     not rounded; rope NULL: k_fresh[j] itself), or v_fresh[j];
+ *   - need = the smallest 2^e, -100 <= e <= 100, with max |x| <= 448 * 2^e over the
+ *     block's fresh rows of a head, infinities and NaN left out; 0 if that is 0;
+ *   - scale = need if every token of the block is fresh, else max(old scale, need);
+ *   - the fresh rows become e4m3(x / scale), round to nearest even (beyond 448: 448;
+ *     NaN stays NaN; scale 0 counts as 1);
+ *   - the block's other rows keep their codes if the scale did not change, else become
+ *     e4m3(code * old / scale): with power-of-two scales that is exact but for values
+ *     below 2^-6 of the new scale, so repeated updates do not drift.
+ * Blocks without an active token keep every byte. A NaN or negative old scale counts
+ * as 0. fresh [cap, H, d] bf16. idx must be ascending and unique; entries out of order,
+ * repeated (the first one counts) or outside [0, N) are skipped or flagged
+ * (TPS_ERR_BOUNDS at tps_check). rope is a HOST pointer. d in {64, 128};
+ * H*d <= 16384; N, cap < 2^31; caches and fresh rows 16-byte aligned. */
+TPS_API int kv_sync_q8(uint8_t* k_cache, uint8_t* v_cache, float* k_scale, float* v_scale, const tps_bf16* k_fresh,
+                       const tps_bf16* v_fresh, const int32_t* idx, const int32_t* count, int64_t cap, int64_t N,
+                       int H, int d, const tps_rope_grid* rope, tps_stream stream);
+
 /* ---- step 5: pruned attention ([HSA] 2.2 (3)-(4); [SVOO] part 2; [TR]) ------
  * For every active row j < min(*count, cap) and head h:
  *   o_act[j,h] = sum_n softmax_n(scale * q_act[j,h] . k[n,h]) v[n,h]
@@ -348,6 +410,28 @@ TPS_API int pruned_attn_mma(const tps_bf16* q_act, const tps_bf16* k, const tps_
                     const int32_t* idx, const int32_t* count, int64_t cap, int64_t N, int H,
                     int d, float scale, const uint8_t* blockmask, int block, tps_bf16* o_act,
                     float* lse, tps_stream stream);
+
+/* pruned_attn over a cache held in 8 bits (the layout of kv_sync_q8):
+ *   o_act[j,h] = sum_n softmax_n(scale * q_act[j,h] . k[n,h]) v[n,h],
+ *   k[n,h] = k_cache[n,h] * k_scale[n / 128][h], v likewise,
+ * with the blockmask, lse and empty-row rules of pruned_attn. Scales must be finite
+ * and >= 0 (a scale of 0 stands for values of 0), the non-zero v_scale within
+ * [2^-100, 2^100]. The codes are used as they are: Q enters the e4m3 products as two
+ * e4m3 parts (exact for channels down to 2^-10 of a row's largest), the
+ * probabilities and V's codes meet in f16, sums are fp32. Key blocks that a mask
+ * leaves out are not read. A NaN code in an attended block makes the rows that
+ * attend it NaN.
+ * ws: device memory of tps_attn_q8_workspace_size(cap, N, H, d) bytes (0 when no key
+ * split is chosen), 16-byte aligned, no initialisation: a dense call whose grid would
+ * leave the GPU partly idle (few active rows, or a mostly empty last wave) runs as
+ * S <= 32 key ranges there, merged by a second launch. With a NULL or smaller
+ * workspace the call runs unsplit. Calls that share a workspace must be ordered
+ * on the GPU. d in {64, 128}; 1 <= H <= 256; N, cap < 2^31. */
+TPS_API int pruned_attn_q8(const tps_bf16* q_act, const uint8_t* k_cache, const uint8_t* v_cache,
+                           const float* k_scale, const float* v_scale, const int32_t* idx, const int32_t* count,
+                           int64_t cap, int64_t N, int H, int d, float scale, const uint8_t* blockmask, int block,
+                           tps_bf16* o_act, float* lse, void* ws, size_t ws_bytes, tps_stream stream);
+TPS_API size_t tps_attn_q8_workspace_size(int64_t cap, int64_t N, int H, int d);
 
 /* ---- attention-recovery merge ([LIPAR] 2.C, log-sum-exp recovery) -------------
  * Exact merge of two attention results over DISJOINT key sets (e.g. two

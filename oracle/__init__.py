@@ -15,9 +15,14 @@ Parity status per function (see each docstring for the pins):
   rope_rotate, kv_rerotate             -- pinned likewise (hand-worked
                                          fixtures, closed forms, invariants,
                                          complex-number form)
+  rope_rows, e4m3_*, q8_*, kv_sync_q8  -- pinned by tests/test_q8_cpu.py
   philox4x32_10 raw stream            -- pinned by the published
                                          known-answer vectors (Salmon et al.,
                                          SC'11), and its normals statistically.
 """
 from .tps_oracle import *  # noqa: F401,F403
 from .tps_oracle import __all__  # noqa: F401
+from .q8_oracle import *  # noqa: F401,F403
+from .q8_oracle import __all__ as _q8_all
+
+__all__ = list(__all__) + list(_q8_all)

@@ -1,0 +1,765 @@
+// pruned_attn_q8: active queries attend all N keys of a cache held in 8 bits
+// (e4m3 codes, one scale for each block of 128 tokens, head and tensor), on the
+// Blackwell tensor cores (tcgen05 + TMEM + TMA).
+//
+// [HSA] 2.2 (3)-(4): the active tokens' queries attend the full cached K/V.
+// [SVOO] part 2: with a mask, a query attends only the 128-key blocks that its
+// ORIGINAL 128-token block keeps.
+//
+// The mathematics, for query row i, key n of block b (a key tile is one scale block):
+//   x = scale log2(e) ks_b (q_i . k8_n),  o_i = sum_n 2^(x - m) vs_b v8_n / sum_n 2^(x - m).
+// Nothing of the cache is dequantised to the scaled value:
+// - Q K^T runs as e4m3 MMAs on the codes. A bf16 value has 8 significant bits and an
+//   e4m3 value 4, so q = 2^e (hi + lo) with hi = e4m3(q / 2^e), lo = e4m3(rest) and one
+//   power of two per row with amax(q) <= 448 * 2^e: exact for channels down to 2^-10 of
+//   the row's largest, and within 2^-18 of the largest below that. Two e4m3 MMAs cost what
+//   one bf16 MMA costs, K stays 8 bits wide in shared memory, and no key is converted.
+// - ks_b enters as the factor of the exponent's FMA. vs_b enters as log2(vs_b) in its
+//   addend, so that P' = 2^(x + log2 vs_b - m) multiplies the codes of V directly; the row
+//   sum takes P' / vs_b. Neither costs an instruction per element.
+// - P' V needs V as wide as P: four converter warps turn the codes into f16 (exact, e4m3 is
+//   a subset of f16) on the way from global to the swizzled shared tile. P' is f16: 11
+//   bits against bf16's 8 make its rounding (2^-11 per probability) vanish beside the
+//   output's. The running maximum is of x + log2 vs_b, so P' <= 2^15 always (kSumLimit);
+//   what underflows is below 2^-25 of the largest P'.
+//
+// Two layouts of a CTA's two 128-row MMA tiles t = 0, 1 (template kOneSet):
+// - false: 256 compacted rows of one head; both tiles consume every K/V tile.
+// - true: one set of at most 128 rows (few active tokens, or the rows of one
+//   query block when a mask is given); tile t takes every second key tile, and the
+//   two partial results are merged through shared memory at the end. A masked row set
+//   streams only the key tiles its query block keeps, so a block that is not kept is
+//   never read, whatever it holds.
+// Warps: 0-3 / 4-7 softmax of tile 0 / 1 (thread r = row r = TMEM lane r), 8-11 converters of V,
+// 12 TMA producer of K, 13 MMA issuer and TMEM owner, 14-15 idle (they complete the
+// warpgroup whose registers go to the softmax). Every mbarrier wait is bounded:
+// on expiry the CTA sets the device status word (TPS_ERR_TIMEOUT), drains what it
+// issued, frees TMEM and returns.
+#include "attn_common.cuh"
+#include "q8.cuh"
+#include "tc_ptx.cuh"
+#include "tma_host.cuh"
+#include "trace.cuh"
+
+namespace tps {
+namespace {
+
+using namespace tc;
+
+constexpr int kBM = 128;        // rows of an MMA tile
+constexpr int kBN = 128;        // keys of a tile = scale block = mask block
+constexpr int kTiles = 2;
+constexpr int kSoftmaxThreads = kTiles * kBM;
+constexpr int kConvThreads = 128;
+constexpr int kThreads = kSoftmaxThreads + kConvThreads + 128;
+constexpr int kConvWarp = kSoftmaxThreads / 32;
+constexpr int kTmaWarp = kConvWarp + kConvThreads / 32;
+constexpr int kMmaWarp = kTmaWarp + 1;
+// 16 warps launch with 128 registers per thread; the warpgroups re-divide them
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 200, kConvRegs = 72, kProducerRegs = 40;
+static_assert(8 * kSoftmaxRegs + 4 * kConvRegs + 4 * kProducerRegs <= 16 * kLaunchRegs, "register split");
+constexpr int kTmemCols = 512;
+constexpr int kListMax = 4096;
+constexpr float kSumLimit = 32768.f;   // largest tile row sum kept without a new maximum: P' stays finite in f16
+static_assert(kBN == kScaleBlock, "a key tile has one scale");
+
+template <int D, bool kOneSet>
+struct Layout {
+  static constexpr int kKStages = D == 64 ? 4 : (kOneSet ? 4 : 3);
+  static constexpr int kVStages = D == 64 ? 4 : 3;
+  static constexpr int kQPart = kBM * D;                 // one e4m3 tile
+  static constexpr int kKTile = kBN * D;
+  static constexpr int kSub = kBN * 128;                 // [128 keys x 64 f16], 128-byte swizzle
+  static constexpr int kVTile = (D / 64) * kSub;
+  static constexpr int kQ = 0;                           // [tile][hi, lo]
+  static constexpr int kV = kQ + (kOneSet ? 1 : kTiles) * 2 * kQPart;
+  static constexpr int kK = kV + kVStages * kVTile;
+  static constexpr int kList = kK + kKStages * kKTile;   // uint16 kept key blocks (kOneSet)
+  static constexpr int kBar = kList + (kOneSet ? 2 * kListMax : 0);
+  static constexpr int kBytes = kBar + 256;
+  static constexpr int kAlloc = kBytes + 1024;           // slack for 1024-byte alignment
+  // mbarrier indices
+  static constexpr int q_full = 0;                       // + tile
+  static constexpr int s_full = q_full + kTiles;         // + tile
+  static constexpr int p_full = s_full + kTiles;         // + tile
+  static constexpr int pv_done = p_full + kTiles;        // + tile
+  static constexpr int k_full = pv_done + kTiles;        // + stage
+  static constexpr int k_empty = k_full + kKStages;
+  static constexpr int v_full = k_empty + kKStages;
+  static constexpr int v_empty = v_full + kVStages;
+  static constexpr int drain = v_empty + kVStages;
+  static_assert((drain + 1) * 8 <= 256, "barrier block");
+  static_assert(kAlloc <= 232448, "shared memory");
+  // the merge of the two tiles stages 128 fp32 rows over the V and K rings
+  static_assert(!kOneSet || kVStages * kVTile + kKStages * kKTile >= kBM * D * 4, "merge staging");
+};
+
+struct Q8Params {
+  AttnArgs a;          // a.k / a.v are not used
+  const uint8_t* v8;
+  const float* ks;
+  const float* vs;
+  float scale_log2;
+  int nsplit;          // key-range splits (blockIdx.z)
+  float* o_part;       // nsplit > 1: normalised fp32 partials [nsplit][cap][H][D] and their
+  float* lse_part;     // log-sum-exp [nsplit][cap][H]
+  unsigned int* status;
+};
+
+__device__ __forceinline__ void barrier_all() { asm volatile("barrier.sync 0;" ::: "memory"); }
+__device__ __forceinline__ void barrier_softmax() {
+  asm volatile("barrier.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// P' = 2^(S * c - base) of one row as f16 pairs; returns the fp32 sum of the unrounded P'.
+__device__ __forceinline__ float exp_row_f16(const uint32_t (&sr)[kBN], float c, float base, uint32_t (&pk)[kBN / 2]) {
+  const uint64_t c2 = f2_pack(c, c), nb2 = f2_pack(-base, -base);
+  uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
+#pragma unroll
+  for (int i = 0; i < kBN; i += 4) {
+    const uint64_t a01 = ffma2(f2_pack(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), c2, nb2);
+    const uint64_t a23 = ffma2(f2_pack(__uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3])), c2, nb2);
+    float a0, a1, a2, a3;
+    f2_unpack(a01, a0, a1);
+    f2_unpack(a23, a2, a3);
+    const float p0 = fast_exp2(a0), p1 = fast_exp2(a1), p2 = fast_exp2(a2), p3 = fast_exp2(a3);
+    acc0 = fadd2(acc0, f2_pack(p0, p1));
+    acc1 = fadd2(acc1, f2_pack(p2, p3));
+    pk[i >> 1] = pack_f16x2(p0, p1);
+    pk[(i >> 1) + 1] = pack_f16x2(p2, p3);
+  }
+  float s0, s1, s2, s3;
+  f2_unpack(acc0, s0, s1);
+  f2_unpack(acc1, s2, s3);
+  return (s0 + s1) + (s2 + s3);
+}
+
+template <int D, bool kOneSet>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ Q8Params prm) {
+  using L = Layout<D, kOneSet>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_row0, s_nrows;
+  __shared__ volatile int s_abort;
+  __shared__ unsigned int s_wcnt[kThreads / 32];
+  __shared__ float2 s_ml[kOneSet ? kBM : 1];
+
+  const AttnArgs& p = prm.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = blockIdx.y;
+  const int64_t rows = active_count(p.count, p.cap);
+  const bool masked = kOneSet && p.bm != nullptr;
+
+  // ---- this CTA's rows: [row0, row0 + nrows) of the compacted queries -----------------------
+  int64_t row0 = static_cast<int64_t>(blockIdx.x) * (kOneSet ? kBM : kTiles * kBM);
+  int nrows = static_cast<int>(rows - row0 < kTiles * kBM ? rows - row0 : kTiles * kBM);
+  if constexpr (kOneSet) {
+    if (masked) {
+      // lanes 0 and 1: lower bounds in idx of this query block and of the next (or of N)
+      if (warp == 0) {
+        int64_t key = (static_cast<int64_t>(blockIdx.x) + (lane & 1)) * kBN;
+        key = key < p.N ? key : p.N;
+        int64_t lo = 0, hi = rows;
+        while (lo < hi) {
+          const int64_t mid = (lo + hi) >> 1;
+          if (p.idx[mid] < key) lo = mid + 1;
+          else hi = mid;
+        }
+        const int64_t n = __shfl_down_sync(0xffffffffu, lo, 1) - lo;
+        if (lane == 0) {
+          s_row0 = static_cast<int>(lo);
+          s_nrows = static_cast<int>(n < 0 ? 0 : (n > kBM ? kBM : n));
+          // more rows than tokens (an index repeated), or entries outside [0, N): those rows are skipped
+          if (h == 0 && (n > kBM || (rows > 0 && blockIdx.x == 0 && (p.idx[0] < 0 || p.idx[rows - 1] >= p.N))))
+            raise_status(prm.status, STATUS_BOUNDS);
+        }
+      }
+      __syncthreads();
+      row0 = s_row0;
+      nrows = s_nrows;
+    } else if (nrows > kBM) {
+      nrows = kBM;
+    }
+  }
+  if (nrows <= 0) return;   // uniform: before TMEM or barriers
+
+  const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (sbase - smem_u32(smem_raw));
+  const uint32_t bar0 = sbase + L::kBar;
+  auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+  uint16_t* sList = reinterpret_cast<uint16_t*>(gbase + L::kList);
+
+  // ---- setup: barriers, TMEM, key tiles ---------------------------------------------------------
+  // active softmax warps of tile t: those with a row; the others have nothing to do
+  const int rows_t0 = nrows < kBM ? nrows : kBM;
+  const int rows_t1 = kOneSet ? rows_t0 : (nrows > kBM ? nrows - kBM : 0);
+  if (tid == 0) {
+    s_abort = 0;
+    for (int t = 0; t < kTiles; ++t) {
+      const int w = ((t ? rows_t1 : rows_t0) + 31) / 32;
+      mbar_init(bar(L::q_full + t), kOneSet ? kSoftmaxThreads : kBM);
+      mbar_init(bar(L::s_full + t), 1);
+      mbar_init(bar(L::p_full + t), 32 * (w > 0 ? w : 1));
+      mbar_init(bar(L::pv_done + t), 1);
+    }
+    for (int s = 0; s < L::kKStages; ++s) {
+      mbar_init(bar(L::k_full + s), 1);
+      mbar_init(bar(L::k_empty + s), 1);
+    }
+    for (int s = 0; s < L::kVStages; ++s) {
+      mbar_init(bar(L::v_full + s), kConvThreads);
+      mbar_init(bar(L::v_empty + s), 1);
+    }
+    mbar_init(bar(L::drain), 1);
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) tmem_alloc<kTmemCols>(smem_u32(&s_tmem));
+  if (warp == kTmaWarp && lane == 0) tma_prefetch_desc(&tmK);
+  const int nkt = static_cast<int>((p.N + kBN - 1) / kBN);
+  // split z covers the key tiles [kt0, kt0 + ntiles)
+  const int kt0 = static_cast<int>((static_cast<int64_t>(nkt) * blockIdx.z) / prm.nsplit);
+  int ntiles = static_cast<int>((static_cast<int64_t>(nkt) * (blockIdx.z + 1)) / prm.nsplit) - kt0;
+  if (masked) {
+    // the key blocks this query block keeps, ascending
+    const uint8_t* mrow = p.bm + static_cast<int64_t>(blockIdx.x) * p.nb;
+    int base = 0;
+    for (int kb0 = 0; kb0 < p.nb; kb0 += kThreads) {
+      const int kb = kb0 + tid;
+      const unsigned int m = __ballot_sync(0xffffffffu, kb < p.nb && mrow[kb] != 0);
+      if (lane == 0) s_wcnt[warp] = __popc(m);
+      __syncthreads();
+      int off = base;
+      for (int i = 0; i < kThreads / 32; ++i) {
+        off += i < warp ? s_wcnt[i] : 0;
+        base += s_wcnt[i];
+      }
+      if ((m >> lane) & 1u) sList[off + __popc(m & ((1u << lane) - 1u))] = static_cast<uint16_t>(kb);
+      __syncthreads();
+    }
+    ntiles = base;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  auto tS = [&](int t) { return tmem + 256u * t; };          // S_t, later P_t (f16 pairs)
+  auto tO = [&](int t) { return tmem + 256u * t + 128u; };   // O_t
+  // the loaded key tiles are numbered q = 0 .. ntiles - 1; step j of tile t reads tile seq(t, j)
+  auto seq = [&](int t, int j) { return kOneSet ? 2 * j + t : j; };
+  auto steps = [&](int t) { return kOneSet ? (ntiles - t + 1) / 2 : ntiles; };
+  auto key_tile = [&](int q) -> int { return masked ? sList[q] : kt0 + q; };
+
+  auto tma_role = [&]() {
+    // ================================ K producer =======================================
+    if (lane == 0) {
+      int issued = 0;
+      for (int q = 0; q < ntiles; ++q) {
+        const int st = q % L::kKStages;
+        if (q >= L::kKStages &&
+            !mbar_wait(bar(L::k_empty + st), ((q / L::kKStages) - 1) & 1, &s_abort, prm.status))
+          break;
+        mbar_expect_tx(bar(L::k_full + st), L::kKTile);
+        tma_load_3d(sbase + L::kK + st * L::kKTile, &tmK, 0, h, key_tile(q) * kBN, bar(L::k_full + st));
+        issued = q + 1;
+      }
+      // every load issued above must land before the CTA may exit
+      for (int q = issued > L::kKStages ? issued - L::kKStages : 0; q < issued; ++q)
+        drain_wait(bar(L::k_full + q % L::kKStages), (q / L::kKStages) & 1);
+    }
+  };
+
+  auto conv_role = [&]() {
+    // ================================ V converters ======================================
+    // kLanes threads hold a key's D codes (16 each); the codes of the next tile are loaded as
+    // those of this one leave the registers.
+    constexpr int kLanes = D / 16;
+    constexpr int kRows = kConvThreads / kLanes;   // keys of one pass
+    constexpr int kPass = kBN / kRows;
+    const int ct = tid - kConvWarp * 32;
+    const int l = ct % kLanes, r0 = ct / kLanes;
+    uint4 buf[kPass];
+    auto load = [&](int q, int i) {
+      const int64_t key = static_cast<int64_t>(key_tile(q)) * kBN + i * kRows + r0;
+      // keys past N become zeros (their P' is 0)
+      buf[i] = key < p.N ? __ldg(reinterpret_cast<const uint4*>(prm.v8 + (key * p.H + h) * D) + l)
+                         : make_uint4(0u, 0u, 0u, 0u);
+    };
+    if (ntiles > 0)
+#pragma unroll
+      for (int i = 0; i < kPass; ++i) load(0, i);
+    for (int q = 0; q < ntiles; ++q) {
+      const int st = q % L::kVStages;
+      if (q >= L::kVStages && !mbar_wait(bar(L::v_empty + st), ((q / L::kVStages) - 1) & 1, &s_abort, prm.status))
+        break;
+      uint8_t* tile = gbase + L::kV + st * L::kVTile;
+#pragma unroll
+      for (int i = 0; i < kPass; ++i) {
+        const int r = i * kRows + r0;
+        const uint4 w = buf[i];
+        if (q + 1 < ntiles) load(q + 1, i);
+        const uint4 a = make_uint4(e4m3x2_to_f16x2(w.x), e4m3x2_to_f16x2(w.x >> 16), e4m3x2_to_f16x2(w.y),
+                                   e4m3x2_to_f16x2(w.y >> 16));
+        const uint4 b = make_uint4(e4m3x2_to_f16x2(w.z), e4m3x2_to_f16x2(w.z >> 16), e4m3x2_to_f16x2(w.w),
+                                   e4m3x2_to_f16x2(w.w >> 16));
+        // channels 16 l .. 16 l + 15 = the 16-byte chunks 2l and 2l + 1; with D = 128 lanes 4-7 (second
+        // 64-channel sub-tile) store theirs in the other order, so 8 lanes cover all banks
+        uint8_t* row = tile + (l / 4) * L::kSub + r * 128;
+        const int c = (2 * l) & 7, odd = l >> 2;
+        *reinterpret_cast<uint4*>(row + (((c + odd) ^ (r & 7)) << 4)) = odd ? b : a;
+        *reinterpret_cast<uint4*>(row + (((c + 1 - odd) ^ (r & 7)) << 4)) = odd ? a : b;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bar(L::v_full + st));
+    }
+  };
+
+  auto mma_role = [&]() {
+    // ================================ MMA issuer =======================================
+    if (lane == 0) {
+      constexpr uint32_t kIdescS = idesc_fmt0(kBM, kBN, false, false);  // e4m3: Q (hi, lo) K^T, both K-major
+      constexpr uint32_t kIdescO = idesc_fmt0(kBM, D, false, true);     // f16: P' V, V is MN-major
+      auto desc = [&](uint32_t a) { return D == 128 ? sdesc_sw128(a, 16, 1024) : sdesc_sw64(a, 16, 512); };
+      auto issue_s = [&](int t, int j) {
+        const int st = seq(t, j) % L::kKStages;
+        const uint32_t qa = sbase + L::kQ + (kOneSet ? 0 : t) * 2 * L::kQPart;
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk)
+            mma_f8_ss(tS(t), desc(qa + part * L::kQPart + kk * 32), desc(sbase + L::kK + st * L::kKTile + kk * 32),
+                      kIdescS, (part > 0 || kk > 0) ? 1u : 0u);
+        mma_commit(bar(L::s_full + t));
+        if (kOneSet || t == kTiles - 1) mma_commit(bar(L::k_empty + st));   // last reader of this stage
+      };
+      auto wait_k = [&](int q) -> bool {
+        return mbar_wait(bar(L::k_full + q % L::kKStages), (q / L::kKStages) & 1, &s_abort, prm.status);
+      };
+      bool ok = true;
+      for (int t = 0; ok && t < kTiles; ++t) {
+        if (steps(t) == 0) continue;
+        ok = mbar_wait(bar(L::q_full + (kOneSet ? 0 : t)), 0, &s_abort, prm.status) && wait_k(seq(t, 0));
+        tc_fence_after();
+        if (ok) issue_s(t, 0);
+      }
+      for (int j = 0; ok && j < steps(0); ++j) {
+        for (int t = 0; ok && t < kTiles; ++t) {
+          if (j >= steps(t)) continue;
+          const int q = seq(t, j), st = q % L::kVStages;
+          ok = mbar_wait(bar(L::p_full + t), j & 1, &s_abort, prm.status);
+          if (ok && (kOneSet || t == 0))
+            ok = mbar_wait(bar(L::v_full + st), (q / L::kVStages) & 1, &s_abort, prm.status);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kBN / 16; ++kk)
+            mma_f16_ts(tO(t), tS(t) + 8 * kk, sdesc_sw128(sbase + L::kV + st * L::kVTile + kk * 16 * 128, L::kSub, 1024),
+                       kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(bar(L::pv_done + t));
+          if (kOneSet || t == kTiles - 1) mma_commit(bar(L::v_empty + st));
+          if (j + 1 < steps(t)) {
+            // S_t(j+1) overwrites the columns P_t(j) was read from: MMAs of one thread run in issue order
+            if (kOneSet || t == 0) {
+              ok = wait_k(seq(t, j + 1));
+              tc_fence_after();
+            }
+            if (ok) issue_s(t, j + 1);
+          }
+        }
+      }
+      mma_commit(bar(L::drain));   // fires once every MMA issued above has completed
+    }
+  };
+
+  auto softmax_role = [&]() {
+    // ================================ softmax warps ====================================
+    const int t = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;         // row of the tile == TMEM lane
+    const int lrow = (kOneSet ? 0 : t * kBM) + r;
+    const bool valid = lrow < nrows;
+    const int64_t row = row0 + lrow;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+
+    // ---- this row of Q as hi + lo e4m3 codes (kOneSet: tile 0's warps store hi, tile 1's lo) ----------
+    float rowc = prm.scale_log2;
+    {
+      constexpr int kVec = D / 8;
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + (row * p.H + h) * D);
+      uint4 x[kVec];
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) x[i] = valid ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float a = fabsf(bf16lo(w[k])), b = fabsf(bf16hi(w[k]));
+          if (a < INFINITY) top = fmaxf(top, a);
+          if (b < INFINITY) top = fmaxf(top, b);
+        }
+      }
+      float sc = scale_of_amax(top);
+      if (sc == 0.f) sc = 1.f;
+      rowc *= sc;
+      const float inv = 1.f / sc;
+      uint8_t* part = gbase + L::kQ + (kOneSet ? 0 : t) * 2 * L::kQPart;
+#pragma unroll
+      for (int i = 0; i < kVec; i += 2) {          // 16 channels = one 16-byte chunk of codes
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint4 v = x[i + (k >> 1)];
+          const uint32_t w[2] = {(k & 1) ? v.z : v.x, (k & 1) ? v.w : v.y};
+          float f[4] = {bf16lo(w[0]) * inv, bf16hi(w[0]) * inv, bf16lo(w[1]) * inv, bf16hi(w[1]) * inv};
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (!(fabsf(f[c]) < INFINITY)) f[c] = NAN;     // an infinite logit makes the row NaN
+          hi[k] = pack_e4m3x4(f[0], f[1], f[2], f[3]);
+          const float2 a = f16x2_to_f2(e4m3x2_to_f16x2(hi[k])), b = f16x2_to_f2(e4m3x2_to_f16x2(hi[k] >> 16));
+          lo[k] = pack_e4m3x4(f[0] - a.x, f[1] - a.y, f[2] - b.x, f[3] - b.y);
+        }
+        const int c = i >> 1;
+        const int off = D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+        if (!kOneSet || t == 0) *reinterpret_cast<uint4*>(part + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if (!kOneSet || t == 1)
+          *reinterpret_cast<uint4*>(part + L::kQPart + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bar(L::q_full + (kOneSet ? 0 : t)));
+    }
+
+    float m_run = -INFINITY, l_run = 0.f;
+    bool ok = true;
+    const int nsteps = steps(t);
+    const bool works = (warp & 3) * 32 < (t ? rows_t1 : rows_t0) || (warp & 3) == 0;
+    auto scales = [&](int j, float& ks, float& vs) {
+      const int64_t at = static_cast<int64_t>(key_tile(seq(t, j))) * p.H + h;
+      ks = __ldg(prm.ks + at);
+      vs = __ldg(prm.vs + at);
+    };
+    float ks_next = 0.f, vs_next = 0.f;
+    if (works && nsteps > 0) scales(0, ks_next, vs_next);
+    for (int j = 0; works && j < nsteps; ++j) {
+      // a scale of 0 (an empty block) stands for values of 0: the smallest positive factors give just that
+      const float c = fmaxf(rowc * ks_next, 1.17549435e-38f);
+      const float vs = fminf(fmaxf(vs_next, 7.8886091e-31f), 1.2676506e30f);   // 2^-100 .. 2^100
+      const float lv = __log2f(vs), ivs = 1.f / vs;
+      if (j + 1 < nsteps) scales(j + 1, ks_next, vs_next);
+      // every wait result is made warp-uniform: tcgen05.ld/st are .sync.aligned
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(L::s_full + t), j & 1, &s_abort, prm.status))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const int64_t key0 = static_cast<int64_t>(key_tile(seq(t, j))) * kBN;
+      const int nvalid = static_cast<int>(p.N - key0 < kBN ? p.N - key0 : kBN);
+      uint32_t sr[kBN];
+      auto load_s = [&]() {
+        tmem_ld64(tS(t) + lane_off, sr);
+        tmem_ld64(tS(t) + lane_off + 64, sr + 64);
+        if (nvalid < kBN) {
+#pragma unroll
+          for (int i = 0; i < kBN; ++i)
+            if (i >= nvalid) sr[i] = __float_as_uint(-INFINITY);
+        }
+      };
+      uint32_t pk[kBN / 2];
+      load_s();
+      // Fast path: keep the running reference. Softmax is exact for any reference; the tile's sum bounds
+      // every P', so P' stays finite in f16 while the sum is at most kSumLimit.
+      bool slow = j == 0;
+      float lt = 0.f;
+      if (!slow) {
+        lt = exp_row_f16(sr, c, m_run - lv, pk);
+        slow = __any_sync(0xffffffffu, !(lt <= kSumLimit));
+        if (slow) load_s();                         // S is intact: P' has not been stored yet
+      }
+      if (slow) {
+        float mx0 = __uint_as_float(sr[0]), mx1 = __uint_as_float(sr[1]);
+        float mx2 = __uint_as_float(sr[2]), mx3 = __uint_as_float(sr[3]);
+#pragma unroll
+        for (int i = 4; i < kBN; i += 4) {
+          mx0 = fmaxf(mx0, __uint_as_float(sr[i]));
+          mx1 = fmaxf(mx1, __uint_as_float(sr[i + 1]));
+          mx2 = fmaxf(mx2, __uint_as_float(sr[i + 2]));
+          mx3 = fmaxf(mx3, __uint_as_float(sr[i + 3]));
+        }
+        // every key tile has a key below N, so the maximum is finite (or S is NaN, and so is the row)
+        const float m_new = fmaxf(m_run, fmaf(fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)), c, lv));
+        if (j == 0) {
+          m_run = m_new;
+        } else if (__any_sync(0xffffffffu, m_new > m_run)) {
+          const float alpha = fast_exp2(m_run - m_new);
+          if (!__all_sync(0xffffffffu, mbar_wait(bar(L::pv_done + t), (j - 1) & 1, &s_abort, prm.status))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int i0 = 0; i0 < D; i0 += 32) {
+            float o[32];
+            tmem_ld32(tO(t) + lane_off + i0, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= alpha;
+            tmem_st32(tO(t) + lane_off + i0, o);
+          }
+          l_run *= alpha;
+          m_run = m_new;
+        }
+        lt = exp_row_f16(sr, c, m_run - lv, pk);
+      }
+      l_run = fmaf(lt, ivs, l_run);
+      tmem_st64(tS(t) + lane_off, pk);            // P'_t(j) over the first 64 columns of S_t
+      tc_fence_before();
+      mbar_arrive(bar(L::p_full + t));
+    }
+    // ---- epilogue ------------------------------------------------------------------------
+    if (ok && nsteps > 0) ok = mbar_wait(bar(L::pv_done + t), (nsteps - 1) & 1, &s_abort, prm.status);
+    ok = __all_sync(0xffffffffu, ok);
+    tc_fence_after();
+    float w0 = 1.f, w1 = 0.f;                     // weights of this tile's and the other tile's sums
+    const float* other = nullptr;
+    if constexpr (kOneSet) {
+      // tile 1 stages its row over the rings (free once both tiles' last products are complete),
+      // chunks rotated by row so the 16-byte accesses of a warp hit distinct banks
+      constexpr int kChunks = D / 4;
+      float4* stage = reinterpret_cast<float4*>(gbase + L::kV);
+      barrier_softmax();
+      if (t == 1 && ok) {
+        s_ml[r] = make_float2(m_run, l_run);
+        if (works && nsteps > 0) {
+#pragma unroll
+          for (int i0 = 0; i0 < D; i0 += 32) {
+            float o[32];
+            tmem_ld32(tO(t) + lane_off + i0, o);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              stage[r * kChunks + (i0 / 4 + q + r) % kChunks] =
+                  make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          }
+        }
+      }
+      barrier_softmax();
+      if (t == 1) return;
+      ok = ok && !s_abort;
+      ok = __all_sync(0xffffffffu, ok);
+      const float2 ml = s_ml[r];
+      const float m = fmaxf(m_run, ml.x);
+      w0 = m_run == -INFINITY ? 0.f : fast_exp2(m_run - m);
+      w1 = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m);
+      l_run = w0 * l_run + (w1 > 0.f ? w1 * ml.y : 0.f);
+      m_run = m;
+      other = reinterpret_cast<const float*>(stage);
+    }
+    if (!ok || !works) return;
+    // a row with no key has l = 0: o = 0, lse = -inf; a NaN sum stays NaN
+    const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+    w0 *= inv;
+    w1 *= inv;
+    const float lse = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
+    const int64_t orow = row * p.H + h;
+    const int64_t prow = prm.nsplit > 1 ? static_cast<int64_t>(blockIdx.z) * p.cap * p.H + orow : 0;
+#pragma unroll
+    for (int i0 = 0; i0 < D; i0 += 32) {
+      float o[32];
+      __syncwarp();
+      if (nsteps > 0) tmem_ld32(tO(t) + lane_off + i0, o);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = nsteps > 0 && l_run != 0.f ? o[i] * w0 : 0.f;
+      if constexpr (kOneSet) {
+        if (w1 != 0.f) {
+          constexpr int kChunks = D / 4;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float4 x = reinterpret_cast<const float4*>(other)[r * kChunks + (i0 / 4 + q + r) % kChunks];
+            o[4 * q] = fmaf(w1, x.x, o[4 * q]);
+            o[4 * q + 1] = fmaf(w1, x.y, o[4 * q + 1]);
+            o[4 * q + 2] = fmaf(w1, x.z, o[4 * q + 2]);
+            o[4 * q + 3] = fmaf(w1, x.w, o[4 * q + 3]);
+          }
+        }
+      }
+      if (valid && prm.nsplit > 1) {
+        float4* dst = reinterpret_cast<float4*>(prm.o_part + prow * D + i0);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+      } else if (valid) {
+        uint4* dst = reinterpret_cast<uint4*>(p.o + orow * D + i0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          dst[q] = make_uint4(pack_bf16x2(o[8 * q], o[8 * q + 1]), pack_bf16x2(o[8 * q + 2], o[8 * q + 3]),
+                              pack_bf16x2(o[8 * q + 4], o[8 * q + 5]), pack_bf16x2(o[8 * q + 6], o[8 * q + 7]));
+      }
+    }
+    if (valid && prm.nsplit > 1) prm.lse_part[prow] = lse;
+    else if (valid && p.lse) p.lse[orow] = lse;
+  };
+
+  // teardown; each role runs its own copy (ptxas allots a region the registers of its setmaxnreg only
+  // if the region does not rejoin the other warps' code)
+  auto tail = [&]() {
+    if (warp == kMmaWarp && lane == 0) drain_wait(bar(L::drain), 0);   // no MMA may still write TMEM
+    tc_fence_before();
+    barrier_all();
+    tc_fence_after();
+    if (warp == kMmaWarp) {
+      __syncwarp();
+      tmem_dealloc<kTmemCols>(tmem);
+    }
+  };
+  if (warp >= kTmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+    if (warp == kTmaWarp) tma_role();
+    else if (warp == kMmaWarp) mma_role();
+    tail();
+  } else if (warp >= kConvWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
+    conv_role();
+    tail();
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    softmax_role();
+    tail();
+  }
+}
+
+// ---- host ------------------------------------------------------------------------------------
+// [N, H, d] e4m3 codes -> 3-D map (d, H, N), box (d, 1, 128): one swizzle row per key.
+int make_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, int64_t N, int H, int d) {
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(N)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H) * d};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(d), 1, kBN};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(TPS_ERR_CUDA, "pruned_attn_q8: cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return TPS_OK;
+}
+
+template <auto kKernel>
+int smem_attribute(int bytes) {
+  static std::atomic<bool> done[64];   // one set per kernel
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const bool cached = dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire);
+  if (!cached) {
+    cudaError_t e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return cuda_status(e, "pruned_attn_q8: smem attribute");
+    if (dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
+  }
+  return TPS_OK;
+}
+
+// How a call runs: the row layout and the key-range split S of a dense call. Cost model in key-tile
+// steps: ceil(units S / SMs) waves of (steps / S + kEnds), kEnds = prologue and epilogue; a split
+// also pays the merge launch. Masked calls are one CTA per query block and head.
+struct Plan {
+  bool one_set;
+  int split;
+};
+constexpr double kEnds = 6.0, kMerge = 3.0;
+constexpr int kMaxSplit = 32;
+
+Plan make_plan(int64_t cap, int64_t N, int H, bool masked) {
+  Plan best{masked || cap <= kBM, 1};
+  if (masked || cap < 1) return best;
+  const int64_t units = (best.one_set ? 1 : (cap + kTiles * kBM - 1) / (kTiles * kBM)) * H;
+  const int64_t nkt = (N + kBN - 1) / kBN;
+  const double steps = best.one_set ? nkt / 2.0 : static_cast<double>(nkt);
+  const int64_t P = sm_count();
+  double cost = 1e300;
+  for (int s = 1; s <= kMaxSplit && (s == 1 || nkt >= 8 * s); ++s) {
+    const double waves = static_cast<double>((units * s + P - 1) / P);
+    const double c = waves * (steps / s + kEnds) + (s > 1 ? kMerge : 0.0);
+    if (c < 0.98 * cost) {
+      cost = c;
+      best.split = s;
+    }
+  }
+  return best;
+}
+
+size_t ws_bytes_of(int split, int64_t cap, int H, int d) {
+  if (split <= 1) return 0;
+  const size_t o = static_cast<size_t>(split) * cap * H * d * sizeof(float);
+  return (o + 255) / 256 * 256 + static_cast<size_t>(split) * cap * H * sizeof(float);
+}
+
+template <int D, bool kOneSet>
+int launch(const CUtensorMap& mk, const Q8Params& prm, cudaStream_t st) {
+  constexpr int kSmem = Layout<D, kOneSet>::kAlloc;
+  if (int e = smem_attribute<attn_q8_kernel<D, kOneSet>>(kSmem)) return e;
+  const int per = kOneSet ? kBM : kTiles * kBM;
+  const int64_t gx = prm.a.bm ? prm.a.nb : (prm.a.cap + per - 1) / per;
+  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(prm.a.H), static_cast<unsigned>(prm.nsplit));
+  attn_q8_kernel<D, kOneSet><<<grid, kThreads, kSmem, st>>>(mk, prm);
+  return launch_status("pruned_attn_q8");
+}
+
+}  // namespace
+
+// S-way merge of the split partials (merge.cu).
+int merge_split_parts(const float* o_part, const float* lse_part, int nsplit, const int32_t* count, int64_t cap,
+                      int H, int d, uint16_t* o, float* lse, cudaStream_t st);
+
+}  // namespace tps
+
+extern "C" size_t tps_attn_q8_workspace_size(int64_t cap, int64_t N, int H, int d) {
+  using namespace tps;
+  if (cap <= 0 || cap >= (INT64_C(1) << 31) || N <= 0 || N >= (INT64_C(1) << 31) || H <= 0 || H > 256 ||
+      (d != 64 && d != 128))
+    return 0;
+  return ws_bytes_of(make_plan(cap, N, H, false).split, cap, H, d);
+}
+
+extern "C" int pruned_attn_q8(const tps_bf16* q_act, const uint8_t* k_cache, const uint8_t* v_cache,
+                              const float* k_scale, const float* v_scale, const int32_t* idx, const int32_t* count,
+                              int64_t cap, int64_t N, int H, int d, float scale, const uint8_t* blockmask, int block,
+                              tps_bf16* o_act, float* lse, void* ws, size_t ws_bytes, tps_stream stream) {
+  TPS_TRACE("pruned_attn_q8");
+  using namespace tps;
+  Q8Params prm{};
+  if (int e = attn_validate("pruned_attn_q8", q_act, reinterpret_cast<const tps_bf16*>(k_cache),
+                            reinterpret_cast<const tps_bf16*>(v_cache), idx, count, cap, N, H, d, scale, blockmask,
+                            block, o_act, lse, &prm.a))
+    return e;
+  if (!k_scale || !v_scale) return fail(TPS_ERR_INVALID_ARG, "pruned_attn_q8: null scales");
+  if ((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale) | reinterpret_cast<uintptr_t>(lse)) & 3u)
+    return fail(TPS_ERR_ALIGN, "pruned_attn_q8: scales and lse must be 4-byte aligned");
+  if (cap == 0) return ok();
+  Plan plan = make_plan(cap, N, H, blockmask != nullptr);
+  if (!ws || !aligned16(ws) || ws_bytes < ws_bytes_of(plan.split, cap, H, d)) plan.split = 1;
+  EncodeTiledFn enc;
+  if (int e = tensor_map_encoder(&enc, "pruned_attn_q8")) return e;
+  int err;
+  prm.status = device_status(&err);
+  if (!prm.status) return err;
+  CUtensorMap mk;
+  if (int e = make_map(enc, &mk, k_cache, N, H, d)) return e;
+  prm.v8 = v_cache;
+  prm.ks = k_scale;
+  prm.vs = v_scale;
+  prm.scale_log2 = scale * kLog2e;
+  prm.nsplit = plan.split;
+  if (plan.split > 1) {
+    prm.o_part = static_cast<float*>(ws);
+    prm.lse_part = reinterpret_cast<float*>(
+        static_cast<char*>(ws) + (static_cast<size_t>(plan.split) * cap * H * d * sizeof(float) + 255) / 256 * 256);
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int e;
+  if (plan.one_set) e = d == 64 ? launch<64, true>(mk, prm, st) : launch<128, true>(mk, prm, st);
+  else e = d == 64 ? launch<64, false>(mk, prm, st) : launch<128, false>(mk, prm, st);
+  if (!e && plan.split > 1)
+    e = merge_split_parts(prm.o_part, prm.lse_part, plan.split, count, cap, H, d, o_act, lse, st);
+  return e ? e : ok();
+}

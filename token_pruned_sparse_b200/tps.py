@@ -8,6 +8,7 @@ fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 
@@ -43,6 +44,12 @@ SIGNATURES = {
     "tps_attn_workspace_size": (C.c_size_t, [_I64, _I64, _INT, _INT]),
     "tps_attn_split": (_INT, [_I64, _I64, _INT, _INT]),
     "tps_attn_plan": (_INT, [_I64, _I64, _INT, _INT, _P, _P, _P]),
+    "tps_rope_table": (_INT, [_P, _P, _P, _P, C.c_float]),
+    "rope_rows": (_INT, [_P, _P, _P, _P, _P, _P, _I64, _I64, _INT, _INT, _P, _INT, _P]),
+    "kv_sync_q8": (_INT, [_P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _INT, _INT, _P, _P]),
+    "pruned_attn_q8": (_INT, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _INT, _INT, C.c_float, _P, _INT, _P, _P, _P,
+                              C.c_size_t, _P]),
+    "tps_attn_q8_workspace_size": (C.c_size_t, [_I64, _I64, _INT, _INT]),
     "pruned_attn_pair": (_INT, [_P, _P, _P, _P, _P, _I64, _I64, _INT, _INT, C.c_float, _P, _INT, _P, _P, _P]),
     "pruned_attn_mma": (_INT, [_P, _P, _P, _P, _P, _I64, _I64, _INT, _INT, C.c_float, _P, _INT, _P, _P, _P]),
     "scatter_out": (_INT, [_P, _P, _P, _P, _I64, _I64, _INT, _INT, _P]),
@@ -307,6 +314,173 @@ def pruned_attn_mma(q_act, k, v, idx, count, scale, blockmask=None, block=128, o
                     cap=None, stream=None):
     return _attn(lib().pruned_attn_mma, q_act, k, v, idx, count, scale, blockmask, block, o_act, lse, cap,
                  stream)
+
+
+# ---- rotary rows and the 8-bit cache --------------------------------------------------
+# These check their tensors on the host (the library sees addresses only) and run on
+# the tensors' device, on its current stream unless one is given.
+def _need(cond, msg, code=INVALID_ARG):
+    if not cond:
+        raise TPSError(code, msg)
+
+
+def _tensor(who, name, t, dtypes, shape, device):
+    _need(isinstance(t, torch.Tensor), f"{who}: {name} must be a tensor")
+    _need(t.dtype in dtypes, f"{who}: {name} is {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    _need(t.device == device, f"{who}: {name} is on {t.device}, expected {device}")
+    _need(t.is_contiguous(), f"{who}: {name} must be contiguous")
+    _need(len(t.shape) == len(shape) and all(w is None or s == w for s, w in zip(t.shape, shape)),
+          f"{who}: {name} has shape {tuple(t.shape)}, expected {tuple('*' if w is None else w for w in shape)}", SHAPE)
+
+
+def _rows(who, idx, count, cap, rows, device):
+    """Checks the active list against the rows at hand; returns cap."""
+    cap = rows if cap is None else int(cap)
+    _need(0 <= cap <= rows, f"{who}: cap={cap} must be in [0, {rows}]", SHAPE)
+    _tensor(who, "idx", idx, (torch.int32,), (None,), device)
+    _tensor(who, "count", count, (torch.int32,), (1,), device)
+    _need(idx.numel() >= cap, f"{who}: idx holds {idx.numel()} entries, cap={cap}", SHAPE)
+    return cap
+
+
+def _call(device, stream, fn, *args):
+    """fn(*args, stream) with the tensors' device current; raises on an error status."""
+    _need(device.type == "cuda", f"{fn.__name__}: tensors are on {device}, expected a CUDA device")
+    with torch.cuda.device(device):
+        _chk(fn(*args, _stream(stream)))
+
+
+class RopeGrid(C.Structure):
+    """tps_rope_grid: channels and positions of the t, x, y axes, and the table."""
+    _fields_ = [("dims", C.c_int32 * 3), ("size", C.c_int32 * 3), ("table", C.c_void_p)]
+
+
+def rope_table(dims, grid, origin=(0, 0, 0), base=10000.0, device=None):
+    """The (cos, sin) table of a latent grid (F, Hs, Ws) for rope_rows and kv_sync_q8:
+    float32 [entries, 2] on `device`, computed on the host in double precision. dims:
+    channels of the t, x, y groups; origin: position of the first token on t, x, y."""
+    F, Hs, Ws = (int(v) for v in grid)
+    size = (F, Ws, Hs)
+    _need(all(s >= 1 for s in size), f"rope_table: grid {tuple(grid)} must be positive", SHAPE)
+    _need(all(int(v) >= 0 and int(v) % 2 == 0 for v in dims), f"rope_table: dims {tuple(dims)} must be even and >= 0")
+    t = torch.empty((sum(s * (int(v) // 2) for s, v in zip(size, dims)), 2), dtype=torch.float32)
+    arr = [C.cast((C.c_int32 * 3)(*[int(v) for v in a]), _P) for a in (dims, size, origin)]
+    _chk(lib().tps_rope_table(_P(t.data_ptr()), *arr, float(base)))
+    return t.to(device or "cuda")
+
+
+def _rope_grid(who, table, dims, grid, device):
+    F, Hs, Ws = (int(v) for v in grid)
+    size = (F, Ws, Hs)
+    dims = [int(v) for v in dims]
+    _need(len(dims) == 3 and all(v >= 0 and v % 2 == 0 for v in dims), f"{who}: dims {dims} must be even and >= 0")
+    _need(min(size) >= 1, f"{who}: grid {tuple(grid)} must be positive", SHAPE)
+    _tensor(who, "table", table, (torch.float32,), (sum(s * (v // 2) for s, v in zip(size, dims)), 2), device)
+    return RopeGrid((C.c_int32 * 3)(*dims), (C.c_int32 * 3)(*size), table.data_ptr())
+
+
+def rope_rows(src, idx, count, table, dims, grid, dst=None, src2=None, dst2=None, inverse=False, cap=None,
+              stream=None):
+    """Rows of src (and src2) [cap, H, d] bf16 turned to the position of token idx[j]
+    on the grid (F, Hs, Ws), or back with inverse=True (the gradient). table:
+    rope_table(dims, grid). idx and count None: row j is token j. Returns dst, or
+    (dst, dst2); dst may be src."""
+    who = "rope_rows"
+    _need(isinstance(src, torch.Tensor) and src.dim() == 3, f"{who}: src must be [rows, H, d]", SHAPE)
+    A, H, d = src.shape
+    dev = src.device
+    if dst is None:
+        dst = torch.empty_like(src)
+    if src2 is not None and dst2 is None:
+        dst2 = torch.empty_like(src2)
+    _need(src2 is not None or dst2 is None, f"{who}: dst2 without src2")
+    for name, t in (("src", src), ("dst", dst), ("src2", src2), ("dst2", dst2)):
+        if t is not None:
+            _tensor(who, name, t, (torch.bfloat16,), (A, H, d), dev)
+    if idx is None:
+        _need(count is None or count.numel() == 1, f"{who}: count must hold one entry", SHAPE)
+        cap = A if cap is None else int(cap)
+        _need(0 <= cap <= A, f"{who}: cap={cap} must be in [0, {A}]", SHAPE)
+        if count is not None:
+            _tensor(who, "count", count, (torch.int32,), (1,), dev)
+    else:
+        cap = _rows(who, idx, count, cap, A, dev)
+    g = _rope_grid(who, table, dims, grid, dev)
+    _call(dev, stream, lib().rope_rows, _ptr(dst), _ptr(src), _ptr(dst2), _ptr(src2), _ptr(idx), _ptr(count), cap,
+          g.size[0] * g.size[1] * g.size[2], H, d, C.cast(C.byref(g), _P), int(bool(inverse)))
+    return dst if src2 is None else (dst, dst2)
+
+
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _cache_q8(who, k_cache, v_cache, k_scale, v_scale):
+    _need(isinstance(k_cache, torch.Tensor) and k_cache.dim() == 3, f"{who}: k_cache must be [N, H, d]", SHAPE)
+    N, H, d = k_cache.shape
+    dev = k_cache.device
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _tensor(who, name, t, _CODES, (N, H, d), dev)
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _tensor(who, name, t, (torch.float32,), ((N + 127) // 128, H), dev)
+    return N, H, d, dev
+
+
+def cache_q8(N, H, d, device=None):
+    """An empty 8-bit cache: (k_cache, v_cache, k_scale, v_scale), e4m3 codes [N, H, d] and
+    float32 scales [ceil(N / 128), H], all zero."""
+    dev = device or "cuda"
+    codes = [torch.zeros((N, H, d), dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn) for _ in range(2)]
+    scales = [torch.zeros(((N + 127) // 128, H), dtype=torch.float32, device=dev) for _ in range(2)]
+    return (*codes, *scales)
+
+
+def kv_sync_q8(k_cache, v_cache, k_scale, v_scale, k_fresh, v_fresh, idx, count, rope=None, cap=None, stream=None):
+    """Fresh K/V rows [cap, H, d] bf16 of the active tokens into the 8-bit cache, in
+    place. rope = (table, dims, grid) turns the keys to their position on the way."""
+    who = "kv_sync_q8"
+    N, H, d, dev = _cache_q8(who, k_cache, v_cache, k_scale, v_scale)
+    for name, t in (("k_fresh", k_fresh), ("v_fresh", v_fresh)):
+        _tensor(who, name, t, (torch.bfloat16,), (None, H, d), dev)
+    cap = _rows(who, idx, count, cap, min(k_fresh.shape[0], v_fresh.shape[0]), dev)
+    g = None if rope is None else _rope_grid(who, *rope, dev)
+    _call(dev, stream, lib().kv_sync_q8, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(k_fresh),
+          _ptr(v_fresh), _ptr(idx), _ptr(count), cap, N, H, d, None if g is None else C.cast(C.byref(g), _P))
+
+
+def attn_q8_workspace(cap, N, H, d, device=None):
+    """The workspace of a dense pruned_attn_q8 call of this shape (its size depends on the
+    device's SM count, so ask on the device that runs it)."""
+    dev = torch.device(device or "cuda")
+    with torch.cuda.device(dev):
+        n = int(lib().tps_attn_q8_workspace_size(int(cap), int(N), int(H), int(d)))
+    return torch.empty(n, dtype=torch.uint8, device=dev)
+
+
+def pruned_attn_q8(q_act, k_cache, v_cache, k_scale, v_scale, idx, count, scale, blockmask=None, block=128,
+                   o_act=None, lse=None, cap=None, ws=None, stream=None):
+    """pruned_attn over the 8-bit cache. ws None: a workspace from torch's allocator, where the
+    call takes one."""
+    who = "pruned_attn_q8"
+    N, H, d, dev = _cache_q8(who, k_cache, v_cache, k_scale, v_scale)
+    _tensor(who, "q_act", q_act, (torch.bfloat16,), (None, H, d), dev)
+    if o_act is None:
+        o_act = torch.empty_like(q_act)
+    _tensor(who, "o_act", o_act, (torch.bfloat16,), (None, H, d), dev)
+    if lse is not None:
+        _tensor(who, "lse", lse, (torch.float32,), (None, H), dev)
+    if blockmask is not None:
+        nb = (N + 127) // 128
+        _tensor(who, "blockmask", blockmask, (torch.uint8, torch.bool), (nb, nb), dev)
+    cap = _rows(who, idx, count, cap, min(t.shape[0] for t in (q_act, o_act, lse) if t is not None), dev)
+    _need(ws is None or (ws.device == dev and ws.is_contiguous()), f"{who}: ws must be contiguous, on {dev}")
+    if ws is None and blockmask is None:
+        on = torch.cuda.current_stream(dev) if stream is None else stream
+        with torch.cuda.stream(on) if hasattr(on, "cuda_stream") else contextlib.nullcontext():
+            ws = attn_q8_workspace(cap, N, H, d, dev)
+    _call(dev, stream, lib().pruned_attn_q8, _ptr(q_act), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+          _ptr(idx), _ptr(count), cap, N, H, d, float(scale), _ptr(blockmask), int(block), _ptr(o_act), _ptr(lse),
+          _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size())
+    return o_act
 
 
 def scatter_out(o_full, o_act, idx, count, cap=None, stream=None):
