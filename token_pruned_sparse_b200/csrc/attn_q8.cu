@@ -76,19 +76,22 @@ struct Layout {
   static constexpr int kK = kV + kVStages * kVTile;
   static constexpr int kList = kK + kKStages * kKTile;   // uint16 kept key blocks (kOneSet)
   static constexpr int kBar = kList + (kOneSet ? 2 * kListMax : 0);
-  static constexpr int kBytes = kBar + 256;
+  static constexpr int kBytes = kBar + 512;
   static constexpr int kAlloc = kBytes + 1024;           // slack for 1024-byte alignment
   // mbarrier indices
   static constexpr int q_full = 0;                       // + tile
   static constexpr int s_full = q_full + kTiles;         // + tile
-  static constexpr int p_full = s_full + kTiles;         // + tile
-  static constexpr int pv_done = p_full + kTiles;        // + tile
-  static constexpr int k_full = pv_done + kTiles;        // + stage
+  // + 2 * tile + half: each has one phase per key tile. (One barrier for both halves would let a warp that
+  // is through with its second half arrive in the place of one that is still at its first.)
+  static constexpr int p_full = s_full + kTiles;
+  static constexpr int pv_done = p_full + 2 * kTiles;
+  static constexpr int k_full = pv_done + 2 * kTiles;    // + stage
   static constexpr int k_empty = k_full + kKStages;
   static constexpr int v_full = k_empty + kKStages;
   static constexpr int v_empty = v_full + kVStages;
-  static constexpr int drain = v_empty + kVStages;
-  static_assert((drain + 1) * 8 <= 256, "barrier block");
+  static constexpr int exp_done = v_empty + kVStages;    // + 4 * tile + warp of the tile
+  static constexpr int drain = exp_done + 4 * kTiles;
+  static_assert((drain + 1) * 8 <= 512, "barrier block");
   static_assert(kAlloc <= 232448, "shared memory");
   // the merge of the two tiles stages 128 fp32 rows over the V and K rings
   static_assert(!kOneSet || kVStages * kVTile + kKStages * kKTile >= kBM * D * 4, "merge staging");
@@ -117,27 +120,22 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-// P' = 2^(S * c - base) of one row as f16 pairs; returns the fp32 sum of the unrounded P'.
-__device__ __forceinline__ float exp_row_f16(const uint32_t (&sr)[kBN], float c, float base, uint32_t (&pk)[kBN / 2]) {
-  const uint64_t c2 = f2_pack(c, c), nb2 = f2_pack(-base, -base);
-  uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
+// P' = 2^(S * c - base) of 32 columns as f16 pairs; the unrounded P' are added to acc.
+__device__ __forceinline__ void exp_cols_f16(const uint32_t (&sr)[32], uint64_t c2, uint64_t nb2, uint32_t* pk,
+                                             uint64_t (&acc)[2]) {
 #pragma unroll
-  for (int i = 0; i < kBN; i += 4) {
+  for (int i = 0; i < 32; i += 4) {
     const uint64_t a01 = ffma2(f2_pack(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), c2, nb2);
     const uint64_t a23 = ffma2(f2_pack(__uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3])), c2, nb2);
     float a0, a1, a2, a3;
     f2_unpack(a01, a0, a1);
     f2_unpack(a23, a2, a3);
     const float p0 = fast_exp2(a0), p1 = fast_exp2(a1), p2 = fast_exp2(a2), p3 = fast_exp2(a3);
-    acc0 = fadd2(acc0, f2_pack(p0, p1));
-    acc1 = fadd2(acc1, f2_pack(p2, p3));
+    acc[0] = fadd2(acc[0], f2_pack(p0, p1));
+    acc[1] = fadd2(acc[1], f2_pack(p2, p3));
     pk[i >> 1] = pack_f16x2(p0, p1);
     pk[(i >> 1) + 1] = pack_f16x2(p2, p3);
   }
-  float s0, s1, s2, s3;
-  f2_unpack(acc0, s0, s1);
-  f2_unpack(acc1, s2, s3);
-  return (s0 + s1) + (s2 + s3);
 }
 
 template <int D, bool kOneSet>
@@ -206,8 +204,10 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       const int w = ((t ? rows_t1 : rows_t0) + 31) / 32;
       mbar_init(bar(L::q_full + t), kOneSet ? kSoftmaxThreads : kBM);
       mbar_init(bar(L::s_full + t), 1);
-      mbar_init(bar(L::p_full + t), 32 * (w > 0 ? w : 1));
-      mbar_init(bar(L::pv_done + t), 1);
+      for (int u = 0; u < 2; ++u) {
+        mbar_init(bar(L::p_full + 2 * t + u), 32 * (w > 0 ? w : 1));
+        mbar_init(bar(L::pv_done + 2 * t + u), 1);
+      }
     }
     for (int s = 0; s < L::kKStages; ++s) {
       mbar_init(bar(L::k_full + s), 1);
@@ -217,6 +217,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       mbar_init(bar(L::v_full + s), kConvThreads);
       mbar_init(bar(L::v_empty + s), 1);
     }
+    for (int w = 0; w < 4 * kTiles; ++w) mbar_init(bar(L::exp_done + w), 1);
     mbar_init(bar(L::drain), 1);
     fence_mbar_init();
   }
@@ -322,21 +323,34 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 
   auto mma_role = [&]() {
     // ================================ MMA issuer =======================================
-    if (lane == 0) {
+    // One thread issues every MMA, so the cycles between two issues count: descriptors are a base
+    // plus a constant in the 14-bit address field (shared memory ends below 2^18 bytes: no carry).
+    if (elect_one()) {
       constexpr uint32_t kIdescS = idesc_fmt0(kBM, kBN, false, false);  // e4m3: Q (hi, lo) K^T, both K-major
       constexpr uint32_t kIdescO = idesc_fmt0(kBM, D, false, true);     // f16: P' V, V is MN-major
-      auto desc = [&](uint32_t a) { return D == 128 ? sdesc_sw128(a, 16, 1024) : sdesc_sw64(a, 16, 512); };
-      auto issue_s = [&](int t, int j) {
-        const int st = seq(t, j) % L::kKStages;
-        const uint32_t qa = sbase + L::kQ + (kOneSet ? 0 : t) * 2 * L::kQPart;
+      auto base = [&](uint32_t a) { return D == 128 ? sdesc_sw128(a, 16, 1024) : sdesc_sw64(a, 16, 512); };
+      const uint64_t dq = base(sbase + L::kQ), dk = base(sbase + L::kK);
+      const uint64_t dv = sdesc_sw128(sbase + L::kV, L::kSub, 1024);
+      auto issue_s = [&](int t, int st) {
+        const uint64_t da = dq + ((kOneSet ? 0 : t) * 2 * L::kQPart >> 4), db = dk + (st * L::kKTile >> 4);
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk)
-            mma_f8_ss(tS(t), desc(qa + part * L::kQPart + kk * 32), desc(sbase + L::kK + st * L::kKTile + kk * 32),
-                      kIdescS, (part > 0 || kk > 0) ? 1u : 0u);
+        for (int i = 0; i < D / 16; ++i) {     // hi parts, then lo parts, 32 channels each
+          const int part = i / (D / 32), kk = i % (D / 32);
+          mma_f8_ss(tS(t), da + ((part * L::kQPart + kk * 32) >> 4), db + (kk * 32 >> 4), kIdescS, i > 0 ? 1u : 0u);
+        }
         mma_commit(bar(L::s_full + t));
         if (kOneSet || t == kTiles - 1) mma_commit(bar(L::k_empty + st));   // last reader of this stage
+      };
+      // O_t += P' V over half u of the tile's keys
+      auto issue_o = [&](int t, int st, int u, bool first) {
+        const uint64_t db = dv + (st * L::kVTile >> 4);
+#pragma unroll
+        for (int i = 0; i < kBN / 32; ++i) {
+          const int kk = u * (kBN / 32) + i;
+          mma_f16_ts(tO(t), tS(t) + 8 * kk, db + (kk * 16 * 128 >> 4), kIdescO, (kk > 0 || !first) ? 1u : 0u);
+        }
+        mma_commit(bar(L::pv_done + 2 * t + u));
+        if (u == 1 && (kOneSet || t == kTiles - 1)) mma_commit(bar(L::v_empty + st));
       };
       auto wait_k = [&](int q) -> bool {
         return mbar_wait(bar(L::k_full + q % L::kKStages), (q / L::kKStages) & 1, &s_abort, prm.status);
@@ -346,35 +360,35 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         if (steps(t) == 0) continue;
         ok = mbar_wait(bar(L::q_full + (kOneSet ? 0 : t)), 0, &s_abort, prm.status) && wait_k(seq(t, 0));
         tc_fence_after();
-        if (ok) issue_s(t, 0);
+        if (ok) issue_s(t, seq(t, 0) % L::kKStages);
       }
       for (int j = 0; ok && j < steps(0); ++j) {
-        for (int t = 0; ok && t < kTiles; ++t) {
-          if (j >= steps(t)) continue;
-          const int q = seq(t, j), st = q % L::kVStages;
-          ok = mbar_wait(bar(L::p_full + t), j & 1, &s_abort, prm.status);
-          if (ok && (kOneSet || t == 0))
-            ok = mbar_wait(bar(L::v_full + st), (q / L::kVStages) & 1, &s_abort, prm.status);
-          if (!ok) break;
-          tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < kBN / 16; ++kk)
-            mma_f16_ts(tO(t), tS(t) + 8 * kk, sdesc_sw128(sbase + L::kV + st * L::kVTile + kk * 16 * 128, L::kSub, 1024),
-                       kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(bar(L::pv_done + t));
-          if (kOneSet || t == kTiles - 1) mma_commit(bar(L::v_empty + st));
+        for (int t = 0; t < kTiles; ++t) {
+          if (!ok || j >= steps(t)) continue;
+          const int q = seq(t, j), st = q % L::kVStages;
+          if (kOneSet || t == 0) ok = mbar_wait(bar(L::v_full + st), (q / L::kVStages) & 1, &s_abort, prm.status);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            ok = ok && mbar_wait(bar(L::p_full + 2 * t + u), j & 1, &s_abort, prm.status);
+            tc_fence_after();
+            if (ok) issue_o(t, st, u, j == 0);
+          }
+          if (!ok) continue;
           if (j + 1 < steps(t)) {
             // S_t(j+1) overwrites the columns P_t(j) was read from: MMAs of one thread run in issue order
+            const int qn = seq(t, j + 1);
             if (kOneSet || t == 0) {
-              ok = wait_k(seq(t, j + 1));
+              ok = wait_k(qn);
               tc_fence_after();
             }
-            if (ok) issue_s(t, j + 1);
+            if (ok) issue_s(t, qn % L::kKStages);
           }
         }
       }
       mma_commit(bar(L::drain));   // fires once every MMA issued above has completed
     }
+    __syncwarp();
   };
 
   auto softmax_role = [&]() {
@@ -438,7 +452,13 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     const int nsteps = steps(t);
-    const bool works = (warp & 3) * 32 < (t ? rows_t1 : rows_t0) || (warp & 3) == 0;
+    auto has_rows = [&](int tile) { return (warp & 3) * 32 < (tile ? rows_t1 : rows_t0) || (warp & 3) == 0; };
+    const bool works = has_rows(t);
+    // The warps w of both tiles share a scheduler and its exp2 unit. They take turns: left alone they
+    // drift into step (each tile's MMAs queue behind the other's) and both wait for the MMAs at once.
+    const bool turns = works && has_rows(1 - t);
+    const uint32_t my_turn_over = bar(L::exp_done + 4 * t + (warp & 3));
+    const uint32_t other_turn_over = bar(L::exp_done + 4 * (1 - t) + (warp & 3));
     auto scales = [&](int j, float& ks, float& vs) {
       const int64_t at = static_cast<int64_t>(key_tile(seq(t, j))) * p.H + h;
       ks = __ldg(prm.ks + at);
@@ -460,68 +480,92 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       tc_fence_after();
       const int64_t key0 = static_cast<int64_t>(key_tile(seq(t, j))) * kBN;
       const int nvalid = static_cast<int>(p.N - key0 < kBN ? p.N - key0 : kBN);
-      uint32_t sr[kBN];
-      auto load_s = [&]() {
-        tmem_ld64(tS(t) + lane_off, sr);
-        tmem_ld64(tS(t) + lane_off + 64, sr + 64);
-        if (nvalid < kBN) {
+      // The tile goes in two halves of 64 keys: the first half's products run while the second half's
+      // exponentials are taken.
+      if (turns && j >= 1 - t &&
+          !__all_sync(0xffffffffu, mbar_wait(other_turn_over, (j - 1 + t) & 1, &s_abort, prm.status)))
+        ok = false;
+      const uint64_t c2 = f2_pack(c, c);
 #pragma unroll
-          for (int i = 0; i < kBN; ++i)
-            if (i >= nvalid) sr[i] = __float_as_uint(-INFINITY);
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t at = tS(t) + lane_off + 64 * u;
+        uint32_t pk[32];
+        uint64_t acc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+        auto sum = [&]() -> float {
+          float x0, x1, x2, x3;
+          f2_unpack(acc[0], x0, x1);
+          f2_unpack(acc[1], x2, x3);
+          return (x0 + x1) + (x2 + x3);
+        };
+        // Fast path: keep the running reference. Softmax is exact for any reference; the half's sum bounds
+        // every P', so P' stays finite in f16 while the sum is at most kSumLimit. S passes through the
+        // registers 32 columns at a time, the next 32 on their way meanwhile: no branch may come between the
+        // two ends of such a load, since the compiler may move registers there that are still to be written.
+        float lt = 0.f;
+        bool slow = (j == 0 && u == 0) || nvalid < kBN;
+        if (!slow) {
+          const uint64_t nb2 = f2_pack(lv - m_run, lv - m_run);
+          uint32_t s0[32], s1[32];
+          tmem_ld32_begin(at, s0);
+          tmem_ld32_end(s0);
+          tmem_ld32_begin(at + 32, s1);
+          exp_cols_f16(s0, c2, nb2, pk, acc);
+          tmem_ld32_end(s1);
+          exp_cols_f16(s1, c2, nb2, pk + 16, acc);
+          lt = sum();
+          slow = __any_sync(0xffffffffu, !(lt <= kSumLimit));
         }
-      };
-      uint32_t pk[kBN / 2];
-      load_s();
-      // Fast path: keep the running reference. Softmax is exact for any reference; the tile's sum bounds
-      // every P', so P' stays finite in f16 while the sum is at most kSumLimit.
-      bool slow = j == 0;
-      float lt = 0.f;
-      if (!slow) {
-        lt = exp_row_f16(sr, c, m_run - lv, pk);
-        slow = __any_sync(0xffffffffu, !(lt <= kSumLimit));
-        if (slow) load_s();                         // S is intact: P' has not been stored yet
-      }
-      if (slow) {
-        float mx0 = __uint_as_float(sr[0]), mx1 = __uint_as_float(sr[1]);
-        float mx2 = __uint_as_float(sr[2]), mx3 = __uint_as_float(sr[3]);
+        if (slow) {                                 // S is intact: P' of this half has not been stored yet
+          uint32_t sr[64];
+          tmem_ld64(at, sr);
+          if (nvalid < kBN) {
 #pragma unroll
-        for (int i = 4; i < kBN; i += 4) {
-          mx0 = fmaxf(mx0, __uint_as_float(sr[i]));
-          mx1 = fmaxf(mx1, __uint_as_float(sr[i + 1]));
-          mx2 = fmaxf(mx2, __uint_as_float(sr[i + 2]));
-          mx3 = fmaxf(mx3, __uint_as_float(sr[i + 3]));
-        }
-        // every key tile has a key below N, so the maximum is finite (or S is NaN, and so is the row)
-        const float m_new = fmaxf(m_run, fmaf(fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)), c, lv));
-        if (j == 0) {
-          m_run = m_new;
-        } else if (__any_sync(0xffffffffu, m_new > m_run)) {
-          const float alpha = fast_exp2(m_run - m_new);
-          if (!__all_sync(0xffffffffu, mbar_wait(bar(L::pv_done + t), (j - 1) & 1, &s_abort, prm.status))) {
-            ok = false;
-            break;
+            for (int i = 0; i < 64; ++i)
+              if (64 * u + i >= nvalid) sr[i] = __float_as_uint(-INFINITY);
           }
-          tc_fence_after();
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i0 = 0; i0 < D; i0 += 32) {
-            float o[32];
-            tmem_ld32(tO(t) + lane_off + i0, o);
+          for (int i = 0; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(sr[i]));
+          // a tile's first half has a key below N, so the first maximum is finite (or S is NaN, and so is
+          // the row)
+          const float m_new = fmaxf(m_run, fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), c, lv));
+          if (j == 0 && u == 0) {
+            m_run = m_new;
+          } else if (__any_sync(0xffffffffu, m_new > m_run)) {
+            // O, complete up to the half before, is rescaled
+            const float alpha = fast_exp2(m_run - m_new);
+            if (!__all_sync(0xffffffffu, mbar_wait(bar(L::pv_done + 2 * t + 1 - u), (j - 1 + u) & 1, &s_abort, prm.status)))
+              ok = false;
+            tc_fence_after();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= alpha;
-            tmem_st32(tO(t) + lane_off + i0, o);
+            for (int i0 = 0; i0 < D; i0 += 16) {    // few registers: sr is held meanwhile
+              float o[16];
+              tmem_ld16(tO(t) + lane_off + i0, o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] *= alpha;
+              tmem_st16(tO(t) + lane_off + i0, o);
+            }
+            l_run *= alpha;
+            m_run = m_new;
           }
-          l_run *= alpha;
-          m_run = m_new;
+          const uint64_t nb2 = f2_pack(lv - m_run, lv - m_run);
+          acc[0] = acc[1] = f2_pack(0.f, 0.f);
+          uint32_t(&lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(sr);
+          uint32_t(&hi)[32] = *reinterpret_cast<uint32_t(*)[32]>(sr + 32);
+          exp_cols_f16(lo, c2, nb2, pk, acc);
+          exp_cols_f16(hi, c2, nb2, pk + 16, acc);
+          lt = sum();
         }
-        lt = exp_row_f16(sr, c, m_run - lv, pk);
+        if (u == 1 && turns && lane == 0) mbar_arrive(my_turn_over);
+        l_run = fmaf(lt, ivs, l_run);
+        tmem_st32_words(tS(t) + lane_off + 32 * u, pk);   // P' over S columns that have been read
+        tc_fence_before();
+        mbar_arrive(bar(L::p_full + 2 * t + u));
       }
-      l_run = fmaf(lt, ivs, l_run);
-      tmem_st64(tS(t) + lane_off, pk);            // P'_t(j) over the first 64 columns of S_t
-      tc_fence_before();
-      mbar_arrive(bar(L::p_full + t));
+      if (!ok) break;
     }
     // ---- epilogue ------------------------------------------------------------------------
-    if (ok && nsteps > 0) ok = mbar_wait(bar(L::pv_done + t), (nsteps - 1) & 1, &s_abort, prm.status);
+    if (ok && nsteps > 0) ok = mbar_wait(bar(L::pv_done + 2 * t + 1), (nsteps - 1) & 1, &s_abort, prm.status);
     ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
     float w0 = 1.f, w1 = 0.f;                     // weights of this tile's and the other tile's sums
@@ -605,7 +649,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   // teardown; each role runs its own copy (ptxas allots a region the registers of its setmaxnreg only
   // if the region does not rejoin the other warps' code)
   auto tail = [&]() {
-    if (warp == kMmaWarp && lane == 0) drain_wait(bar(L::drain), 0);   // no MMA may still write TMEM
+    if (warp == kMmaWarp) drain_wait(bar(L::drain), 0);   // no MMA may still write TMEM
     tc_fence_before();
     barrier_all();
     tc_fence_after();

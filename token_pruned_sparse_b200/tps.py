@@ -8,7 +8,6 @@ fallback.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 import os
 
@@ -318,36 +317,67 @@ def pruned_attn_mma(q_act, k, v, idx, count, scale, blockmask=None, block=128, o
 
 # ---- rotary rows and the 8-bit cache --------------------------------------------------
 # These check their tensors on the host (the library sees addresses only) and run on
-# the tensors' device, on its current stream unless one is given.
+# the tensors' device, on its current stream unless one is given. A call costs the host
+# about 10 us, so a check that passes builds no message, and addresses go to ctypes as ints.
+_T, _BF16, _F32, _I32 = torch.Tensor, torch.bfloat16, torch.float32, torch.int32
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+_MASKS = (torch.uint8, torch.bool)
+_I3 = C.c_int32 * 3
+
+
 def _need(cond, msg, code=INVALID_ARG):
     if not cond:
         raise TPSError(code, msg)
 
 
-def _tensor(who, name, t, dtypes, shape, device):
-    _need(isinstance(t, torch.Tensor), f"{who}: {name} must be a tensor")
+def _refuse(who, name, t, dtypes, shape, index):
+    """Raises what is wrong with a tensor that _check did not take."""
+    _need(isinstance(t, _T), f"{who}: {name} must be a tensor")
+    dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
     _need(t.dtype in dtypes, f"{who}: {name} is {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
-    _need(t.device == device, f"{who}: {name} is on {t.device}, expected {device}")
+    _need(tuple(t.shape) == tuple(shape), f"{who}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}", SHAPE)
+    _need(index >= 0 and t.get_device() == index,
+          f"{who}: {name} is on {t.device}, expected {'a CUDA device' if index < 0 else f'cuda:{index}'}")
     _need(t.is_contiguous(), f"{who}: {name} must be contiguous")
-    _need(len(t.shape) == len(shape) and all(w is None or s == w for s, w in zip(t.shape, shape)),
-          f"{who}: {name} has shape {tuple(t.shape)}, expected {tuple('*' if w is None else w for w in shape)}", SHAPE)
 
 
-def _rows(who, idx, count, cap, rows, device):
-    """Checks the active list against the rows at hand; returns cap."""
+def _check(who, name, t, dtype, shape, index):
+    """t: a contiguous tensor of that type (or of one of them) and shape on CUDA device `index`; returns its address."""
+    if not (isinstance(t, _T) and (t.dtype is dtype or (type(dtype) is tuple and t.dtype in dtype)) and t.shape == shape
+            and t.get_device() == index >= 0 and t.is_contiguous()):
+        _refuse(who, name, t, dtype, shape, index)
+    return t.data_ptr()
+
+
+def _rows_of(who, name, t, H, d):
+    _need(isinstance(t, _T) and t.dim() == 3, f"{who}: {name} must be a [rows, H, d] tensor", SHAPE)
+    return t.shape[0]
+
+
+def _active(who, idx, count, cap, rows, index):
+    """Checks the active list against the rows at hand; returns (cap, address of idx, address of count)."""
     cap = rows if cap is None else int(cap)
-    _need(0 <= cap <= rows, f"{who}: cap={cap} must be in [0, {rows}]", SHAPE)
-    _tensor(who, "idx", idx, (torch.int32,), (None,), device)
-    _tensor(who, "count", count, (torch.int32,), (1,), device)
-    _need(idx.numel() >= cap, f"{who}: idx holds {idx.numel()} entries, cap={cap}", SHAPE)
-    return cap
+    if not 0 <= cap <= rows:
+        raise TPSError(SHAPE, f"{who}: cap={cap} must be in [0, {rows}]")
+    _need(isinstance(idx, _T) and idx.dim() == 1, f"{who}: idx must be a one-dimensional tensor")
+    if idx.shape[0] < cap:
+        raise TPSError(SHAPE, f"{who}: idx holds {idx.shape[0]} entries, cap={cap}")
+    return (cap, _check(who, "idx", idx, _I32, idx.shape, index), _check(who, "count", count, _I32, (1,), index))
 
 
-def _call(device, stream, fn, *args):
-    """fn(*args, stream) with the tensors' device current; raises on an error status."""
-    _need(device.type == "cuda", f"{fn.__name__}: tensors are on {device}, expected a CUDA device")
-    with torch.cuda.device(device):
-        _chk(fn(*args, _stream(stream)))
+def _call(fn, index, stream, *args):
+    """fn(*args, stream) with CUDA device `index` current; raises on an error status."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch.cuda.current_device() == index:
+        code = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            code = fn(*args, raw)
+    if code != OK:
+        _chk(code)
 
 
 class RopeGrid(C.Structure):
@@ -364,19 +394,18 @@ def rope_table(dims, grid, origin=(0, 0, 0), base=10000.0, device=None):
     _need(all(s >= 1 for s in size), f"rope_table: grid {tuple(grid)} must be positive", SHAPE)
     _need(all(int(v) >= 0 and int(v) % 2 == 0 for v in dims), f"rope_table: dims {tuple(dims)} must be even and >= 0")
     t = torch.empty((sum(s * (int(v) // 2) for s, v in zip(size, dims)), 2), dtype=torch.float32)
-    arr = [C.cast((C.c_int32 * 3)(*[int(v) for v in a]), _P) for a in (dims, size, origin)]
+    arr = [C.cast(_I3(*[int(v) for v in a]), _P) for a in (dims, size, origin)]
     _chk(lib().tps_rope_table(_P(t.data_ptr()), *arr, float(base)))
     return t.to(device or "cuda")
 
 
-def _rope_grid(who, table, dims, grid, device):
-    F, Hs, Ws = (int(v) for v in grid)
-    size = (F, Ws, Hs)
-    dims = [int(v) for v in dims]
-    _need(len(dims) == 3 and all(v >= 0 and v % 2 == 0 for v in dims), f"{who}: dims {dims} must be even and >= 0")
-    _need(min(size) >= 1, f"{who}: grid {tuple(grid)} must be positive", SHAPE)
-    _tensor(who, "table", table, (torch.float32,), (sum(s * (v // 2) for s, v in zip(size, dims)), 2), device)
-    return RopeGrid((C.c_int32 * 3)(*dims), (C.c_int32 * 3)(*size), table.data_ptr())
+def _rope_grid(who, table, dims, grid, index):
+    F, Hs, Ws = grid
+    dt, dx, dy = dims
+    if min(dt, dx, dy) < 0 or (dt | dx | dy) & 1 or min(F, Hs, Ws) < 1:
+        raise TPSError(INVALID_ARG, f"{who}: dims {tuple(dims)} must be even and >= 0, grid {tuple(grid)} positive")
+    at = _check(who, "table", table, _F32, (F * (dt // 2) + Ws * (dx // 2) + Hs * (dy // 2), 2), index)
+    return RopeGrid(_I3(dt, dx, dy), _I3(F, Ws, Hs), at)
 
 
 def rope_rows(src, idx, count, table, dims, grid, dst=None, src2=None, dst2=None, inverse=False, cap=None,
@@ -386,43 +415,47 @@ def rope_rows(src, idx, count, table, dims, grid, dst=None, src2=None, dst2=None
     rope_table(dims, grid). idx and count None: row j is token j. Returns dst, or
     (dst, dst2); dst may be src."""
     who = "rope_rows"
-    _need(isinstance(src, torch.Tensor) and src.dim() == 3, f"{who}: src must be [rows, H, d]", SHAPE)
-    A, H, d = src.shape
-    dev = src.device
+    _need(isinstance(src, _T) and src.dim() == 3, "rope_rows: src must be a [rows, H, d] tensor", SHAPE)
+    shape = src.shape
+    A, H, d = shape
+    dev = src.get_device()
+    a_src = _check(who, "src", src, _BF16, shape, dev)
     if dst is None:
         dst = torch.empty_like(src)
-    if src2 is not None and dst2 is None:
-        dst2 = torch.empty_like(src2)
-    _need(src2 is not None or dst2 is None, f"{who}: dst2 without src2")
-    for name, t in (("src", src), ("dst", dst), ("src2", src2), ("dst2", dst2)):
-        if t is not None:
-            _tensor(who, name, t, (torch.bfloat16,), (A, H, d), dev)
+    a_dst = _check(who, "dst", dst, _BF16, shape, dev)
+    a_src2 = a_dst2 = None
+    if src2 is not None:
+        a_src2 = _check(who, "src2", src2, _BF16, shape, dev)
+        if dst2 is None:
+            dst2 = torch.empty_like(src2)
+        a_dst2 = _check(who, "dst2", dst2, _BF16, shape, dev)
+    elif dst2 is not None:
+        raise TPSError(INVALID_ARG, "rope_rows: dst2 without src2")
     if idx is None:
-        _need(count is None or count.numel() == 1, f"{who}: count must hold one entry", SHAPE)
-        cap = A if cap is None else int(cap)
-        _need(0 <= cap <= A, f"{who}: cap={cap} must be in [0, {A}]", SHAPE)
-        if count is not None:
-            _tensor(who, "count", count, (torch.int32,), (1,), dev)
+        cap, a_idx = A if cap is None else int(cap), None
+        _need(0 <= cap <= A, "rope_rows: cap must be in [0, rows of src]", SHAPE)
+        a_cnt = None if count is None else _check(who, "count", count, _I32, (1,), dev)
     else:
-        cap = _rows(who, idx, count, cap, A, dev)
+        cap, a_idx, a_cnt = _active(who, idx, count, cap, A, dev)
+    if cap == 0:
+        return dst if src2 is None else (dst, dst2)
     g = _rope_grid(who, table, dims, grid, dev)
-    _call(dev, stream, lib().rope_rows, _ptr(dst), _ptr(src), _ptr(dst2), _ptr(src2), _ptr(idx), _ptr(count), cap,
-          g.size[0] * g.size[1] * g.size[2], H, d, C.cast(C.byref(g), _P), int(bool(inverse)))
+    F, Hs, Ws = grid
+    _call(lib().rope_rows, dev, stream, a_dst, a_src, a_dst2, a_src2, a_idx, a_cnt, cap, F * Hs * Ws, H, d,
+          C.addressof(g), 1 if inverse else 0)
     return dst if src2 is None else (dst, dst2)
 
 
-_CODES = (torch.uint8, torch.float8_e4m3fn)
-
-
 def _cache_q8(who, k_cache, v_cache, k_scale, v_scale):
-    _need(isinstance(k_cache, torch.Tensor) and k_cache.dim() == 3, f"{who}: k_cache must be [N, H, d]", SHAPE)
-    N, H, d = k_cache.shape
-    dev = k_cache.device
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _tensor(who, name, t, _CODES, (N, H, d), dev)
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _tensor(who, name, t, (torch.float32,), ((N + 127) // 128, H), dev)
-    return N, H, d, dev
+    """Checks a cache; returns its sizes, device index and addresses."""
+    _need(isinstance(k_cache, _T) and k_cache.dim() == 3, "the 8-bit k_cache must be a [N, H, d] tensor", SHAPE)
+    shape = k_cache.shape
+    N, H, d = shape
+    dev = k_cache.get_device()
+    nb = (N + 127) // 128
+    return (N, H, d, dev, _check(who, "k_cache", k_cache, _CODES, shape, dev),
+            _check(who, "v_cache", v_cache, _CODES, shape, dev), _check(who, "k_scale", k_scale, _F32, (nb, H), dev),
+            _check(who, "v_scale", v_scale, _F32, (nb, H), dev))
 
 
 def cache_q8(N, H, d, device=None):
@@ -438,13 +471,16 @@ def kv_sync_q8(k_cache, v_cache, k_scale, v_scale, k_fresh, v_fresh, idx, count,
     """Fresh K/V rows [cap, H, d] bf16 of the active tokens into the 8-bit cache, in
     place. rope = (table, dims, grid) turns the keys to their position on the way."""
     who = "kv_sync_q8"
-    N, H, d, dev = _cache_q8(who, k_cache, v_cache, k_scale, v_scale)
-    for name, t in (("k_fresh", k_fresh), ("v_fresh", v_fresh)):
-        _tensor(who, name, t, (torch.bfloat16,), (None, H, d), dev)
-    cap = _rows(who, idx, count, cap, min(k_fresh.shape[0], v_fresh.shape[0]), dev)
+    N, H, d, dev, a_kc, a_vc, a_ks, a_vs = _cache_q8(who, k_cache, v_cache, k_scale, v_scale)
+    nk, nv = _rows_of(who, "k_fresh", k_fresh, H, d), _rows_of(who, "v_fresh", v_fresh, H, d)
+    a_kf = _check(who, "k_fresh", k_fresh, _BF16, (nk, H, d), dev)
+    a_vf = _check(who, "v_fresh", v_fresh, _BF16, (nv, H, d), dev)
+    cap, a_idx, a_cnt = _active(who, idx, count, cap, min(nk, nv), dev)
+    if cap == 0:
+        return
     g = None if rope is None else _rope_grid(who, *rope, dev)
-    _call(dev, stream, lib().kv_sync_q8, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(k_fresh),
-          _ptr(v_fresh), _ptr(idx), _ptr(count), cap, N, H, d, None if g is None else C.cast(C.byref(g), _P))
+    _call(lib().kv_sync_q8, dev, stream, a_kc, a_vc, a_ks, a_vs, a_kf, a_vf, a_idx, a_cnt, cap, N, H, d,
+          None if g is None else C.addressof(g))
 
 
 def attn_q8_workspace(cap, N, H, d, device=None):
@@ -461,25 +497,47 @@ def pruned_attn_q8(q_act, k_cache, v_cache, k_scale, v_scale, idx, count, scale,
     """pruned_attn over the 8-bit cache. ws None: a workspace from torch's allocator, where the
     call takes one."""
     who = "pruned_attn_q8"
-    N, H, d, dev = _cache_q8(who, k_cache, v_cache, k_scale, v_scale)
-    _tensor(who, "q_act", q_act, (torch.bfloat16,), (None, H, d), dev)
+    N, H, d, dev, a_kc, a_vc, a_ks, a_vs = _cache_q8(who, k_cache, v_cache, k_scale, v_scale)
+    rows = _rows_of(who, "q_act", q_act, H, d)
+    a_q = _check(who, "q_act", q_act, _BF16, (rows, H, d), dev)
     if o_act is None:
         o_act = torch.empty_like(q_act)
-    _tensor(who, "o_act", o_act, (torch.bfloat16,), (None, H, d), dev)
+    n = _rows_of(who, "o_act", o_act, H, d)
+    a_o = _check(who, "o_act", o_act, _BF16, (n, H, d), dev)
+    rows = min(rows, n)
+    a_lse = a_mask = a_ws = None
     if lse is not None:
-        _tensor(who, "lse", lse, (torch.float32,), (None, H), dev)
+        _need(isinstance(lse, _T) and lse.dim() == 2, "pruned_attn_q8: lse must be a [rows, H] tensor", SHAPE)
+        n = lse.shape[0]
+        a_lse = _check(who, "lse", lse, _F32, (n, H), dev)
+        rows = min(rows, n)
     if blockmask is not None:
         nb = (N + 127) // 128
-        _tensor(who, "blockmask", blockmask, (torch.uint8, torch.bool), (nb, nb), dev)
-    cap = _rows(who, idx, count, cap, min(t.shape[0] for t in (q_act, o_act, lse) if t is not None), dev)
-    _need(ws is None or (ws.device == dev and ws.is_contiguous()), f"{who}: ws must be contiguous, on {dev}")
-    if ws is None and blockmask is None:
-        on = torch.cuda.current_stream(dev) if stream is None else stream
-        with torch.cuda.stream(on) if hasattr(on, "cuda_stream") else contextlib.nullcontext():
-            ws = attn_q8_workspace(cap, N, H, d, dev)
-    _call(dev, stream, lib().pruned_attn_q8, _ptr(q_act), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-          _ptr(idx), _ptr(count), cap, N, H, d, float(scale), _ptr(blockmask), int(block), _ptr(o_act), _ptr(lse),
-          _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size())
+        a_mask = _check(who, "blockmask", blockmask, _MASKS, (nb, nb), dev)
+    cap, a_idx, a_cnt = _active(who, idx, count, cap, rows, dev)
+    if cap == 0:
+        return o_act
+    n_ws = 0
+    if ws is not None:
+        n_ws = ws.numel() * ws.element_size()
+        a_ws = _check(who, "ws", ws, ws.dtype, ws.shape, dev)
+    elif blockmask is None:
+        if torch.cuda.current_device() == dev:
+            n_ws = lib().tps_attn_q8_workspace_size(cap, N, H, d)
+        else:
+            with torch.cuda.device(dev):
+                n_ws = lib().tps_attn_q8_workspace_size(cap, N, H, d)
+        if n_ws:
+            # the allocator hands the block on in the order of the current stream: for another stream
+            # it has to be told that the block is in use there
+            ws = torch.empty(n_ws, dtype=torch.uint8, device=q_act.device)
+            a_ws = ws.data_ptr()
+            if stream is not None:
+                on = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), dev)
+                on.wait_stream(torch.cuda.current_stream(dev))
+                ws.record_stream(on)
+    _call(lib().pruned_attn_q8, dev, stream, a_q, a_kc, a_vc, a_ks, a_vs, a_idx, a_cnt, cap, N, H, d, scale, a_mask,
+          block, a_o, a_lse, a_ws, n_ws)
     return o_act
 
 
