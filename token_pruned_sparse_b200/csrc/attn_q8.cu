@@ -80,17 +80,16 @@ struct Layout {
   static constexpr int kAlloc = kBytes + 1024;           // slack for 1024-byte alignment
   // mbarrier indices
   static constexpr int q_full = 0;                       // + tile
-  static constexpr int s_full = q_full + kTiles;         // + tile
   // + 2 * tile + half: each has one phase per key tile. (One barrier for both halves would let a warp that
   // is through with its second half arrive in the place of one that is still at its first.)
-  static constexpr int p_full = s_full + kTiles;
+  static constexpr int s_full = q_full + kTiles;
+  static constexpr int p_full = s_full + 2 * kTiles;
   static constexpr int pv_done = p_full + 2 * kTiles;
   static constexpr int k_full = pv_done + 2 * kTiles;    // + stage
   static constexpr int k_empty = k_full + kKStages;
   static constexpr int v_full = k_empty + kKStages;
   static constexpr int v_empty = v_full + kVStages;
-  static constexpr int exp_done = v_empty + kVStages;    // + 4 * tile + warp of the tile
-  static constexpr int drain = exp_done + 4 * kTiles;
+  static constexpr int drain = v_empty + kVStages;
   static_assert((drain + 1) * 8 <= 512, "barrier block");
   static_assert(kAlloc <= 232448, "shared memory");
   // the merge of the two tiles stages 128 fp32 rows over the V and K rings
@@ -203,8 +202,8 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     for (int t = 0; t < kTiles; ++t) {
       const int w = ((t ? rows_t1 : rows_t0) + 31) / 32;
       mbar_init(bar(L::q_full + t), kOneSet ? kSoftmaxThreads : kBM);
-      mbar_init(bar(L::s_full + t), 1);
       for (int u = 0; u < 2; ++u) {
+        mbar_init(bar(L::s_full + 2 * t + u), 1);
         mbar_init(bar(L::p_full + 2 * t + u), 32 * (w > 0 ? w : 1));
         mbar_init(bar(L::pv_done + 2 * t + u), 1);
       }
@@ -217,7 +216,6 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       mbar_init(bar(L::v_full + s), kConvThreads);
       mbar_init(bar(L::v_empty + s), 1);
     }
-    for (int w = 0; w < 4 * kTiles; ++w) mbar_init(bar(L::exp_done + w), 1);
     mbar_init(bar(L::drain), 1);
     fence_mbar_init();
   }
@@ -250,8 +248,9 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  auto tS = [&](int t) { return tmem + 256u * t; };          // S_t, later P_t (f16 pairs)
-  auto tO = [&](int t) { return tmem + 256u * t + 128u; };   // O_t
+  // S_t of half u of a key tile (64 keys); P'_t (f16 pairs) later takes its first 32 columns
+  auto tS = [&](int t, int u) { return tmem + 256u * t + 64u * u; };
+  auto tO = [&](int t) { return tmem + 256u * t + 128u; };
   // the loaded key tiles are numbered q = 0 .. ntiles - 1; step j of tile t reads tile seq(t, j)
   auto seq = [&](int t, int j) { return kOneSet ? 2 * j + t : j; };
   auto steps = [&](int t) { return kOneSet ? (ntiles - t + 1) / 2 : ntiles; };
@@ -326,63 +325,63 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     // One thread issues every MMA, so the cycles between two issues count: descriptors are a base
     // plus a constant in the 14-bit address field (shared memory ends below 2^18 bytes: no carry).
     if (elect_one()) {
-      constexpr uint32_t kIdescS = idesc_fmt0(kBM, kBN, false, false);  // e4m3: Q (hi, lo) K^T, both K-major
-      constexpr uint32_t kIdescO = idesc_fmt0(kBM, D, false, true);     // f16: P' V, V is MN-major
+      constexpr uint32_t kIdescS = idesc_fmt0(kBM, kBN / 2, false, false);  // e4m3: Q (hi, lo) K^T, both K-major
+      constexpr uint32_t kIdescO = idesc_fmt0(kBM, D, false, true);         // f16: P' V, V is MN-major
       auto base = [&](uint32_t a) { return D == 128 ? sdesc_sw128(a, 16, 1024) : sdesc_sw64(a, 16, 512); };
       const uint64_t dq = base(sbase + L::kQ), dk = base(sbase + L::kK);
       const uint64_t dv = sdesc_sw128(sbase + L::kV, L::kSub, 1024);
-      auto issue_s = [&](int t, int st) {
-        const uint64_t da = dq + ((kOneSet ? 0 : t) * 2 * L::kQPart >> 4), db = dk + (st * L::kKTile >> 4);
+      auto issue_s = [&](int t, int u, int st) {
+        const uint64_t da = dq + ((kOneSet ? 0 : t) * 2 * L::kQPart >> 4);
+        const uint64_t db = dk + ((st * L::kKTile + u * (L::kKTile / 2)) >> 4);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {     // hi parts, then lo parts, 32 channels each
           const int part = i / (D / 32), kk = i % (D / 32);
-          mma_f8_ss(tS(t), da + ((part * L::kQPart + kk * 32) >> 4), db + (kk * 32 >> 4), kIdescS, i > 0 ? 1u : 0u);
+          mma_f8_ss(tS(t, u), da + ((part * L::kQPart + kk * 32) >> 4), db + (kk * 32 >> 4), kIdescS, i > 0 ? 1u : 0u);
         }
-        mma_commit(bar(L::s_full + t));
-        if (kOneSet || t == kTiles - 1) mma_commit(bar(L::k_empty + st));   // last reader of this stage
+        mma_commit(bar(L::s_full + 2 * t + u));
+        if (u == 1 && (kOneSet || t == kTiles - 1)) mma_commit(bar(L::k_empty + st));   // last reader of this stage
       };
-      // O_t += P' V over half u of the tile's keys
-      auto issue_o = [&](int t, int st, int u, bool first) {
-        const uint64_t db = dv + (st * L::kVTile >> 4);
+      auto issue_o = [&](int t, int u, int st, bool first) {
+        const uint64_t db = dv + ((st * L::kVTile + u * 64 * 128) >> 4);
 #pragma unroll
-        for (int i = 0; i < kBN / 32; ++i) {
-          const int kk = u * (kBN / 32) + i;
-          mma_f16_ts(tO(t), tS(t) + 8 * kk, db + (kk * 16 * 128 >> 4), kIdescO, (kk > 0 || !first) ? 1u : 0u);
-        }
+        for (int kk = 0; kk < kBN / 32; ++kk)
+          mma_f16_ts(tO(t), tS(t, u) + 8 * kk, db + (kk * 16 * 128 >> 4), kIdescO, (u > 0 || kk > 0 || !first) ? 1u : 0u);
         mma_commit(bar(L::pv_done + 2 * t + u));
         if (u == 1 && (kOneSet || t == kTiles - 1)) mma_commit(bar(L::v_empty + st));
       };
       auto wait_k = [&](int q) -> bool {
         return mbar_wait(bar(L::k_full + q % L::kKStages), (q / L::kKStages) & 1, &s_abort, prm.status);
       };
+      auto wait_v = [&](int q) -> bool {
+        return mbar_wait(bar(L::v_full + q % L::kVStages), (q / L::kVStages) & 1, &s_abort, prm.status);
+      };
       bool ok = true;
-      for (int t = 0; ok && t < kTiles; ++t) {
-        if (steps(t) == 0) continue;
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        if (!ok || steps(t) == 0) continue;
         ok = mbar_wait(bar(L::q_full + (kOneSet ? 0 : t)), 0, &s_abort, prm.status) && wait_k(seq(t, 0));
         tc_fence_after();
-        if (ok) issue_s(t, seq(t, 0) % L::kKStages);
+        if (!ok) continue;
+        issue_s(t, 0, seq(t, 0) % L::kKStages);
+        issue_s(t, 1, seq(t, 0) % L::kKStages);
       }
+      // Step j: for each half and tile O_t += P'_t V, and S_t of that half of the next key tile in its place
+      // (it overwrites the columns P'_t was read from: MMAs of one thread run in issue order). While a
+      // softmax warp is at one half, the MMAs of its other half run.
       for (int j = 0; ok && j < steps(0); ++j) {
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-          if (!ok || j >= steps(t)) continue;
-          const int q = seq(t, j), st = q % L::kVStages;
-          if (kOneSet || t == 0) ok = mbar_wait(bar(L::v_full + st), (q / L::kVStages) & 1, &s_abort, prm.status);
+        for (int u = 0; u < 2; ++u) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            ok = ok && mbar_wait(bar(L::p_full + 2 * t + u), j & 1, &s_abort, prm.status);
+          for (int t = 0; t < kTiles; ++t) {
+            if (!ok || j >= steps(t)) continue;
+            const int q = seq(t, j), qn = seq(t, j + 1);
+            const bool more = j + 1 < steps(t);
+            if (u == 0 && (kOneSet || t == 0)) ok = wait_v(q) && (!more || wait_k(qn));
+            ok = ok && mbar_spin(bar(L::p_full + 2 * t + u), j & 1, &s_abort, prm.status);
+            if (!ok) continue;
             tc_fence_after();
-            if (ok) issue_o(t, st, u, j == 0);
-          }
-          if (!ok) continue;
-          if (j + 1 < steps(t)) {
-            // S_t(j+1) overwrites the columns P_t(j) was read from: MMAs of one thread run in issue order
-            const int qn = seq(t, j + 1);
-            if (kOneSet || t == 0) {
-              ok = wait_k(qn);
-              tc_fence_after();
-            }
-            if (ok) issue_s(t, qn % L::kKStages);
+            issue_o(t, u, q % L::kVStages, j == 0);
+            if (more) issue_s(t, u, qn % L::kKStages);
           }
         }
       }
@@ -452,13 +451,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     const int nsteps = steps(t);
-    auto has_rows = [&](int tile) { return (warp & 3) * 32 < (tile ? rows_t1 : rows_t0) || (warp & 3) == 0; };
-    const bool works = has_rows(t);
-    // The warps w of both tiles share a scheduler and its exp2 unit. They take turns: left alone they
-    // drift into step (each tile's MMAs queue behind the other's) and both wait for the MMAs at once.
-    const bool turns = works && has_rows(1 - t);
-    const uint32_t my_turn_over = bar(L::exp_done + 4 * t + (warp & 3));
-    const uint32_t other_turn_over = bar(L::exp_done + 4 * (1 - t) + (warp & 3));
+    const bool works = (warp & 3) * 32 < (t ? rows_t1 : rows_t0) || (warp & 3) == 0;
     auto scales = [&](int j, float& ks, float& vs) {
       const int64_t at = static_cast<int64_t>(key_tile(seq(t, j))) * p.H + h;
       ks = __ldg(prm.ks + at);
@@ -472,23 +465,20 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       const float vs = fminf(fmaxf(vs_next, 7.8886091e-31f), 1.2676506e30f);   // 2^-100 .. 2^100
       const float lv = __log2f(vs), ivs = 1.f / vs;
       if (j + 1 < nsteps) scales(j + 1, ks_next, vs_next);
-      // every wait result is made warp-uniform: tcgen05.ld/st are .sync.aligned
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(L::s_full + t), j & 1, &s_abort, prm.status))) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
       const int64_t key0 = static_cast<int64_t>(key_tile(seq(t, j))) * kBN;
       const int nvalid = static_cast<int>(p.N - key0 < kBN ? p.N - key0 : kBN);
-      // The tile goes in two halves of 64 keys: the first half's products run while the second half's
-      // exponentials are taken.
-      if (turns && j >= 1 - t &&
-          !__all_sync(0xffffffffu, mbar_wait(other_turn_over, (j - 1 + t) & 1, &s_abort, prm.status)))
-        ok = false;
+      // The tile goes in two halves of 64 keys, each with its own S: the MMAs of one half run while the
+      // exponentials of the other are taken.
       const uint64_t c2 = f2_pack(c, c);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const uint32_t at = tS(t) + lane_off + 64 * u;
+        // every wait result is made warp-uniform: tcgen05.ld/st are .sync.aligned
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(L::s_full + 2 * t + u), j & 1, &s_abort, prm.status))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t at = tS(t, u) + lane_off;
         uint32_t pk[32];
         uint64_t acc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
         auto sum = [&]() -> float {
@@ -556,9 +546,8 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
           exp_cols_f16(hi, c2, nb2, pk + 16, acc);
           lt = sum();
         }
-        if (u == 1 && turns && lane == 0) mbar_arrive(my_turn_over);
         l_run = fmaf(lt, ivs, l_run);
-        tmem_st32_words(tS(t) + lane_off + 32 * u, pk);   // P' over S columns that have been read
+        tmem_st32_words(at, pk);                    // P' over S columns that have been read
         tc_fence_before();
         mbar_arrive(bar(L::p_full + 2 * t + u));
       }
