@@ -14,17 +14,15 @@
 // range below (steps of 2^-9 of the scale); repeated updates do not drift.
 //
 // HBM-bound: 2 bytes read and 1 written per fresh element. A CTA takes one block of 128
-// tokens of one tensor, for a run of heads: it finds the block's part of the ascending
-// idx with two warp searches, lists its tokens and, for keys, gathers their (cos, sin)
-// entries into shared memory. Then each warp takes a head: it loads all of the head's
-// fresh rows of the block into registers at once (16 bytes per lane, up to 32 loads in
-// flight, 64 rows of 128 or 128 rows of 64 channels) and goes over them once: turn,
-// maximum, and codes against the OLD scale, which is the new one as long as the block
-// got no louder. Only where the scale changes are the rows loaded again (from L2)
-// and encoded again. No warp waits for another, except with more than 64 rows of 128
-// channels: then two warps share a head and exchange their maxima. What it measured at
-// the HSA size: CTA-wide passes of 128 (row, head) slots with three barriers each 466
-// us; this layout with two turns from the table in global memory 375 us.
+// tokens of one tensor (and of a run of heads, where blocks alone would not fill the GPU):
+// it finds the block's part of the ascending idx with two warp searches, lists its tokens
+// and, for keys, gathers their (cos, sin) entries into shared memory. Then it streams the
+// rows once: a warp takes 512 contiguous bytes of each of a part of the rows, 8 loads in
+// flight, turns them, keeps the maximum, and writes the codes against the OLD scale, which
+// is the new one as long as the block got no louder. Heads whose scale does change are
+// read again (from L2) and encoded again. Measured at the HSA size (0.73 GB): CTA-wide passes
+// of 128 (row, head) slots with the block's values held in registers 466 us, a warp holding
+// its head's rows 210-220 us, this 155 us (3 CTAs per SM of 80 registers instead of 2 of 116: 173).
 #include <climits>
 
 #include "q8.cuh"
@@ -35,10 +33,12 @@
 namespace tps {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kVecs = 32;        // 16-byte vectors per lane in registers
-constexpr int kCtasWanted = 24;  // CTAs of a launch per SM (3 run at a time)
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kUnroll = 8;       // rows of a warp in flight
+constexpr int kPart = 16;        // rows of one task: a block's tasks spread evenly over the warps
+constexpr int kMaxHeads = 256;
+constexpr int kCtasWanted = 6;   // CTAs of a launch per SM (2 run at a time)
 
 struct SyncQ8 {
   uint8_t* cache[2];
@@ -49,7 +49,8 @@ struct SyncQ8 {
   int64_t cap;
   int64_t N;
   int H;
-  int heads;       // heads per CTA
+  int vpr;         // 16-byte vectors of a fresh row
+  int groups;      // 32-vector groups per CTA
   RopeGrid grid;
   unsigned int* status;
 };
@@ -80,21 +81,17 @@ __device__ __forceinline__ uint2 codes_of(const float (&v)[8], float inv) {
                     pack_e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
 }
 __device__ __forceinline__ float factor_of(float scale) { return scale > 0.f ? 1.f / scale : 1.f; }
-// Largest of the non-negative floats of a warp.
-__device__ __forceinline__ float warp_max(float x) {
-  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
-}
 
 template <int D, bool kTurn>
 __device__ __forceinline__ void sync_block(const SyncQ8& p, int tensor) {
-  constexpr int kLanes = D / 8;              // lanes of a row, 8 channels each
-  constexpr int kRows = 32 / kLanes;         // rows of one warp-wide vector
-  constexpr int kHeld = kVecs * kRows;       // rows a warp holds
+  constexpr int kLanes = D / 8;              // lanes of a head's row, 8 channels each
+  constexpr int kHeads = 32 / kLanes;        // heads of a 32-vector group
   __shared__ int64_t s_run[2];
   __shared__ int s_src[kScaleBlock];     // fresh row of each token of the block, or INT_MAX
   __shared__ int2 s_list[kScaleBlock];   // (token of the block, fresh row), ascending
-  __shared__ int s_cnt[kWarps];
-  __shared__ float s_top[kWarps];
+  __shared__ int s_cnt[kScaleBlock / 32];
+  __shared__ int s_top[kMaxHeads];       // bits of each head's maximum (non-negative floats order as ints)
+  __shared__ float s_was[kMaxHeads], s_inv[kMaxHeads];
   extern __shared__ float4 s_cs[];       // kTurn: (cos, sin) of two pairs per entry, D / 4 entries per listed token
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -105,7 +102,7 @@ __device__ __forceinline__ void sync_block(const SyncQ8& p, int tensor) {
     const int64_t at = warp_lower_bound(p.idx, cnt, n0 + warp * kScaleBlock, lane);
     if (lane == 0) s_run[warp] = at;
   }
-  s_src[tid] = INT_MAX;
+  if (tid < kScaleBlock) s_src[tid] = INT_MAX;
   __syncthreads();
   const int64_t lo = s_run[0], hi = s_run[1];
   if (blockIdx.y == 0 && tensor == 0 && tid == 0 && cnt > 0 &&
@@ -114,6 +111,10 @@ __device__ __forceinline__ void sync_block(const SyncQ8& p, int tensor) {
   if (hi <= lo) return;
 
   const int size = static_cast<int>(p.N - n0 < kScaleBlock ? p.N - n0 : kScaleBlock);
+  const int g0 = blockIdx.y * p.groups;                          // this CTA's groups and heads
+  const int ng = min(p.groups, (p.vpr + 31) / 32 - g0);
+  const int h0 = g0 * kHeads, nh = min(ng * kHeads, p.H - h0);
+  float* scale = p.scale[tensor] + b * p.H + h0;
   for (int64_t j = lo + tid; j < hi; j += kThreads) {
     const int64_t n = static_cast<int64_t>(p.idx[j]) - n0;
     const bool in = n >= 0 && n < size;
@@ -121,134 +122,162 @@ __device__ __forceinline__ void sync_block(const SyncQ8& p, int tensor) {
     // out of order, outside [0, N) or a repeated token
     if (!in || (j > lo && p.idx[j - 1] >= p.idx[j])) raise_status(p.status, STATUS_BOUNDS);
   }
+  if (tid < nh) {
+    s_top[tid] = 0;
+    s_was[tid] = scale[tid];
+    s_inv[tid] = factor_of(s_was[tid]);
+  }
   __syncthreads();
-  static_assert(kThreads == kScaleBlock, "one thread per token of the block");
-  const unsigned int mine = __ballot_sync(0xffffffffu, s_src[tid] != INT_MAX);
-  if (lane == 0) s_cnt[warp] = __popc(mine);
+  unsigned int mine = 0;
+  if (tid < kScaleBlock) {
+    mine = __ballot_sync(0xffffffffu, s_src[tid] != INT_MAX);
+    if (lane == 0) s_cnt[warp] = __popc(mine);
+  }
   __syncthreads();
-  int nact = 0, before = 0;
+  int nact = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    before += w < warp ? s_cnt[w] : 0;
+  for (int w = 0; w < kScaleBlock / 32; ++w) {
+    if (w == warp && ((mine >> lane) & 1u))
+      s_list[nact + __popc(mine & ((1u << lane) - 1u))] = make_int2(tid, s_src[tid]);
     nact += s_cnt[w];
   }
-  if ((mine >> lane) & 1u) s_list[before + __popc(mine & ((1u << lane) - 1u))] = make_int2(tid, s_src[tid]);
   __syncthreads();
   if (nact == 0) return;
   const bool whole = nact == size;
   if constexpr (kTurn) {
-    // a quarter-warp's worth of threads per token: 4 pairs each
     for (int i = tid; i < nact * kLanes; i += kThreads) {
       const int c = i / kLanes, l = i % kLanes;
       float2 e[4];
       rope_lookup(p.grid, static_cast<uint32_t>(n0) + s_list[c].x, l * 4, e);
-      s_cs[(c * kLanes + l) * 2] = make_float4(e[0].x, e[0].y, e[1].x, e[1].y);
-      s_cs[(c * kLanes + l) * 2 + 1] = make_float4(e[2].x, e[2].y, e[3].x, e[3].y);
+      s_cs[i * 2] = make_float4(e[0].x, e[0].y, e[1].x, e[1].y);
+      s_cs[i * 2 + 1] = make_float4(e[2].x, e[2].y, e[3].x, e[3].y);
     }
     __syncthreads();
   }
 
-  const int lane8 = lane % kLanes, sub = lane / kLanes;
   const uint4* fresh = reinterpret_cast<const uint4*>(p.fresh[tensor]);
   uint2* cache = reinterpret_cast<uint2*>(p.cache[tensor]);
-  float* scale = p.scale[tensor] + b * p.H;
-  const int hend = min(p.H, (static_cast<int>(blockIdx.y) + 1) * p.heads);
-  const int share = nact > kHeld ? 2 : 1;              // warps per head
-  const int c0 = share == 2 ? (warp & 1) * kHeld : 0;  // this warp's first row in the list
-  const int mylen = min(nact - c0, kHeld);
+  const int lane8 = lane % kLanes;
+  const int ntasks = ng * ((nact + kPart - 1) / kPart);
+  // A task is one group of one part of the rows; f(v, head, first row, end) with this lane's vector v.
+  auto tasks = [&](auto&& f) {
+    for (int k = warp; k < ntasks; k += kWarps) {
+      const int g = k % ng, c0 = k / ng * kPart;
+      const int v = (g0 + g) * 32 + lane;
+      f(v, g * kHeads + lane / kLanes, c0, min(c0 + kPart, nact));
+    }
+  };
+  auto load = [&](int v, int c) { return fresh[static_cast<int64_t>(s_list[c].y) * p.vpr + v]; };
+  auto entries = [&](int c) { return s_cs + (c * kLanes + lane8) * 2; };
+  auto store = [&](int v, int c, uint2 o) { cache[(n0 + s_list[c].x) * p.vpr + v] = o; };
+  auto largest = [](const float(&x)[8]) {
+    float a = fmaxf(fabsf(x[0]), fabsf(x[1]));           // (NaN is passed over)
+#pragma unroll
+    for (int q = 2; q < 8; ++q) a = fmaxf(a, fabsf(x[q]));
+    return a;
+  };
+  auto keep_top = [&](float top, int head, bool on) {
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (on && lane8 == 0) atomicMax(&s_top[head], __float_as_int(top));
+  };
 
-  for (int h0 = blockIdx.y * p.heads; h0 < hend; h0 += kWarps / share) {
-    const int h = h0 + warp / share;
-    const bool on = h < hend;
-    auto row_of = [&](int c) { return fresh + (static_cast<int64_t>(s_list[c0 + c].y) * p.H + h) * kLanes + lane8; };
-    auto entries = [&](int c) { return s_cs + ((c0 + c) * kLanes + lane8) * 2; };
-    auto place = [&](int c) { return cache + ((n0 + s_list[c0 + c].x) * p.H + h) * kLanes + lane8; };
-    uint4 x[kVecs];
-    if (on) {
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i)
-        if (i * kRows + sub < mylen) x[i] = *row_of(i * kRows + sub);
-    }
-    const float was = on ? scale[h] : 0.f;
-    const float inv_was = factor_of(was);
+  // ---- one pass: codes against the old scale, and the maxima -----------------------------------
+  tasks([&](int v, int head, int c0, int c1) {
+    const bool on = v < p.vpr;
+    const float inv = on ? s_inv[head] : 1.f;
     float top = 0.f;
-    if (on) {
+    for (int c = c0; c < c1; c += kUnroll) {
+      uint4 x[kUnroll];
 #pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        const int c = i * kRows + sub;
-        if (c < mylen) {
-          float v[8];
-          values_of<kTurn>(x[i], entries(c), v);
+      for (int u = 0; u < kUnroll; ++u)     // rows behind the last repeat it: the same codes to the same place
+        if (on) x[u] = load(v, min(c + u, c1 - 1));
+      if (on) {
 #pragma unroll
-          for (int q = 0; q < 8; ++q) top = fmaxf(top, fabsf(v[q]));   // (NaN is passed over)
-          const uint2 o = codes_of(v, inv_was);
-          x[i].x = o.x;
-          x[i].y = o.y;
+        for (int u = 0; u < kUnroll; ++u) {
+          float f[8];
+          values_of<kTurn>(x[u], entries(min(c + u, c1 - 1)), f);
+          top = fmaxf(top, largest(f));
+          store(v, min(c + u, c1 - 1), codes_of(f, inv));
         }
       }
-      top = warp_max(top);
-      if (top == INFINITY) {                           // infinities set no scale: look again without them
-        top = 0.f;
-#pragma unroll 1
-        for (int c = sub; c < mylen; c += kRows) {
-          float v[8];
-          values_of<kTurn>(*row_of(c), entries(c), v);
+    }
+    keep_top(top, head, on);
+  });
+  __syncthreads();
+
+  // ---- the new scales -------------------------------------------------------------------------------
+  bool infinite = tid < nh && s_top[tid] == 0x7F800000;
+  if (__syncthreads_or(infinite)) {         // infinities set no scale: look again without them
+    if (infinite) s_top[tid] = 0;
+    __syncthreads();
+    tasks([&](int v, int head, int c0, int c1) {
+      const bool on = v < p.vpr;
+      float top = 0.f;
+      for (int c = c0; on && c < c1; ++c) {
+        float f[8];
+        values_of<kTurn>(load(v, c), entries(c), f);
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            if (fabsf(v[q]) < INFINITY) top = fmaxf(top, fabsf(v[q]));
-        }
-        top = warp_max(top);
+        for (int q = 0; q < 8; ++q)
+          if (fabsf(f[q]) < INFINITY) top = fmaxf(top, fabsf(f[q]));
       }
+      keep_top(top, head, on);
+    });
+    __syncthreads();
+  }
+  bool changed = false;
+  float ratio = 0.f;
+  if (tid < nh) {
+    const float was = s_was[tid], need = scale_of_amax(__int_as_float(s_top[tid]));
+    const float sc = whole ? need : fmaxf(need, was);     // a NaN old scale counts as none
+    changed = !(sc == was);
+    if (changed) {
+      scale[tid] = sc;
+      ratio = !(was > 0.f) ? 0.f : was / sc;
+      s_inv[tid] = factor_of(sc);
     }
-    if (share == 2) {                                  // uniform over the CTA
-      __syncthreads();
-      if (lane == 0) s_top[warp] = top;
-      __syncthreads();
-      top = fmaxf(s_top[warp], s_top[warp ^ 1]);
-    }
-    if (!on) continue;                                 // no barrier from here to the next head's
-    const float need = scale_of_amax(top);
-    const float sc = whole ? need : fmaxf(need, was);  // a NaN old scale counts as none
-    if (sc == was) {
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i)
-        if (i * kRows + sub < mylen) *place(i * kRows + sub) = make_uint2(x[i].x, x[i].y);
-    } else {
-      const float inv = factor_of(sc);
+    s_top[tid] = changed;
+    s_was[tid] = ratio;
+  }
+  if (!__syncthreads_or(changed)) return;
+
+  // ---- the heads whose scale changed: fresh rows again, and the stale ones --------------------------
+  tasks([&](int v, int head, int c0, int c1) {
+    if (v >= p.vpr || !s_top[head]) return;
+    const float inv = s_inv[head];
 #pragma unroll 4
-      for (int c = sub; c < mylen; c += kRows) {
-        float v[8];
-        values_of<kTurn>(*row_of(c), entries(c), v);
-        *place(c) = codes_of(v, inv);
-      }
+    for (int c = c0; c < c1; ++c) {
+      float f[8];
+      values_of<kTurn>(load(v, c), entries(c), f);
+      store(v, c, codes_of(f, inv));
     }
-    if (share == 1 || (warp & 1) == 0) {
-      if (!whole && (sc > was || was != was)) {        // the scale grew: the stale rows move to it
-        const float ratio = was > 0.f ? was / sc : 0.f;
+  });
+  if (whole) return;
+  for (int k = warp; k < ng * (kScaleBlock / kPart); k += kWarps) {
+    const int g = k % ng, r0 = k / ng * kPart;
+    const int v = (g0 + g) * 32 + lane, head = g * kHeads + lane / kLanes;
+    if (v >= p.vpr || !s_top[head]) continue;
+    const float r = s_was[head];
 #pragma unroll 4
-        for (int r = sub; r < size; r += kRows) {
-          if (s_src[r] != INT_MAX) continue;
-          uint2* at = cache + ((n0 + r) * p.H + h) * kLanes + lane8;
-          const uint2 w = *at;
-          uint32_t o[2];
+    for (int n = r0; n < min(r0 + kPart, size); ++n) {
+      if (s_src[n] != INT_MAX) continue;
+      uint2* at = cache + (n0 + n) * p.vpr + v;
+      const uint2 w = *at;
+      uint32_t o[2];
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const uint32_t u = q ? w.y : w.x;
-            const float2 e = f16x2_to_f2(e4m3x2_to_f16x2(u)), f = f16x2_to_f2(e4m3x2_to_f16x2(u >> 16));
-            o[q] = pack_e4m3x4(e.x * ratio, e.y * ratio, f.x * ratio, f.y * ratio);
-          }
-          *at = make_uint2(o[0], o[1]);
-        }
+      for (int q = 0; q < 2; ++q) {
+        const uint32_t u = q ? w.y : w.x;
+        const float2 e = f16x2_to_f2(e4m3x2_to_f16x2(u)), f = f16x2_to_f2(e4m3x2_to_f16x2(u >> 16));
+        o[q] = pack_e4m3x4(e.x * r, e.y * r, f.x * r, f.y * r);
       }
-      __syncwarp();
-      if (lane == 0) scale[h] = sc;                    // (a second warp of the head read the old one before its barrier)
+      *at = make_uint2(o[0], o[1]);
     }
   }
 }
 
 // blockIdx.z: 0 = K, 1 = V
 template <int D, bool kTurnK>
-__global__ void __launch_bounds__(kThreads, 3) sync_q8_kernel(const __grid_constant__ SyncQ8 p) {
+__global__ void __launch_bounds__(kThreads, 2) sync_q8_kernel(const __grid_constant__ SyncQ8 p) {
   if (kTurnK && blockIdx.z == 0) sync_block<D, true>(p, 0);
   else sync_block<D, false>(p, blockIdx.z);
 }
@@ -292,14 +321,14 @@ extern "C" int kv_sync_q8(uint8_t* k_cache, uint8_t* v_cache, float* k_scale, fl
   p.N = N;
   p.H = H;
   const int64_t nb = (N + kScaleBlock - 1) / kScaleBlock;
-  // Heads per CTA: every CTA pays the search of its run, so it takes several heads per warp where the
-  // blocks fill the GPU; small caches spread over the heads instead.
+  // Every CTA pays the search of its run and the gathering of its entries, so it takes all heads where the
+  // blocks alone fill the GPU; small caches spread over the heads instead.
+  p.vpr = H * (d / 8);
+  const int64_t all = (p.vpr + 31) / 32;
   int64_t chunks = (static_cast<int64_t>(sm_count()) * kCtasWanted + 2 * nb - 1) / (2 * nb);
-  const int64_t most = (H + kWarps - 1) / kWarps;
-  chunks = chunks < 1 ? 1 : (chunks > most ? most : chunks);
-  p.heads = static_cast<int>((H + chunks - 1) / chunks);
-  p.heads = (p.heads + kWarps - 1) / kWarps * kWarps;
-  const dim3 grid(static_cast<unsigned>(nb), static_cast<unsigned>((H + p.heads - 1) / p.heads), 2);
+  chunks = chunks < 1 ? 1 : (chunks > all ? all : chunks);
+  p.groups = static_cast<int>((all + chunks - 1) / chunks);
+  const dim3 grid(static_cast<unsigned>(nb), static_cast<unsigned>((all + p.groups - 1) / p.groups), 2);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const size_t smem = rope ? static_cast<size_t>(kScaleBlock) * (d / 2) * sizeof(float2) : 0;
   if (d == 128 && rope) {
