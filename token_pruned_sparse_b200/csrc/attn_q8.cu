@@ -40,6 +40,7 @@
 #include "tc_ptx.cuh"
 #include "tma_host.cuh"
 #include "trace.cuh"
+#include "warp_search.cuh"
 
 namespace tps {
 namespace {
@@ -56,7 +57,7 @@ constexpr int kConvWarp = kSoftmaxThreads / 32;
 constexpr int kTmaWarp = kConvWarp + kConvThreads / 32;
 constexpr int kMmaWarp = kTmaWarp + 1;
 // 16 warps launch with 128 registers per thread; the warpgroups re-divide them
-constexpr int kLaunchRegs = 128, kSoftmaxRegs = 200, kConvRegs = 72, kProducerRegs = 40;
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 152, kConvRegs = 96, kProducerRegs = 112;
 static_assert(8 * kSoftmaxRegs + 4 * kConvRegs + 4 * kProducerRegs <= 16 * kLaunchRegs, "register split");
 constexpr int kTmemCols = 512;
 constexpr int kListMax = 4096;
@@ -65,8 +66,11 @@ static_assert(kBN == kScaleBlock, "a key tile has one scale");
 
 template <int D, bool kOneSet>
 struct Layout {
-  static constexpr int kKStages = D == 64 ? 4 : (kOneSet ? 4 : 3);
-  static constexpr int kVStages = D == 64 ? 4 : 3;
+  static constexpr int kKStages = D == 64 ? 4 : 3;
+  static constexpr int kVStages = D == 64 ? 4 : (kOneSet ? 2 : 3);
+  // kOneSet: V's codes come through a ring of their own, so that enough bytes are in flight to stream a
+  // long cache for few rows (one tile ahead in the converters' registers reached 2.2 TB/s)
+  static constexpr int kCStages = kOneSet ? (D == 64 ? 6 : 4) : 0;
   static constexpr int kQPart = kBM * D;                 // one e4m3 tile
   static constexpr int kKTile = kBN * D;
   static constexpr int kSub = kBN * 128;                 // [128 keys x 64 f16], 128-byte swizzle
@@ -74,7 +78,8 @@ struct Layout {
   static constexpr int kQ = 0;                           // [tile][hi, lo]
   static constexpr int kV = kQ + (kOneSet ? 1 : kTiles) * 2 * kQPart;
   static constexpr int kK = kV + kVStages * kVTile;
-  static constexpr int kList = kK + kKStages * kKTile;   // uint16 kept key blocks (kOneSet)
+  static constexpr int kC = kK + kKStages * kKTile;      // V's codes
+  static constexpr int kList = kC + kCStages * kKTile;   // uint16 kept key blocks (kOneSet)
   static constexpr int kBar = kList + (kOneSet ? 2 * kListMax : 0);
   static constexpr int kBytes = kBar + 512;
   static constexpr int kAlloc = kBytes + 1024;           // slack for 1024-byte alignment
@@ -89,7 +94,9 @@ struct Layout {
   static constexpr int k_empty = k_full + kKStages;
   static constexpr int v_full = k_empty + kKStages;
   static constexpr int v_empty = v_full + kVStages;
-  static constexpr int drain = v_empty + kVStages;
+  static constexpr int c_full = v_empty + kVStages;
+  static constexpr int c_empty = c_full + kCStages;
+  static constexpr int drain = c_empty + kCStages;
   static_assert((drain + 1) * 8 <= 512, "barrier block");
   static_assert(kAlloc <= 232448, "shared memory");
   // the merge of the two tiles stages 128 fp32 rows over the V and K rings
@@ -139,7 +146,8 @@ __device__ __forceinline__ void exp_cols_f16(const uint32_t (&sr)[32], uint64_t 
 
 template <int D, bool kOneSet>
 __global__ void __launch_bounds__(kThreads, 1)
-attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ Q8Params prm) {
+attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+               const __grid_constant__ Q8Params prm) {
   using L = Layout<D, kOneSet>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
@@ -159,17 +167,11 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   int nrows = static_cast<int>(rows - row0 < kTiles * kBM ? rows - row0 : kTiles * kBM);
   if constexpr (kOneSet) {
     if (masked) {
-      // lanes 0 and 1: lower bounds in idx of this query block and of the next (or of N)
+      // lower bounds in idx of this query block and of the next (or of N)
       if (warp == 0) {
-        int64_t key = (static_cast<int64_t>(blockIdx.x) + (lane & 1)) * kBN;
-        key = key < p.N ? key : p.N;
-        int64_t lo = 0, hi = rows;
-        while (lo < hi) {
-          const int64_t mid = (lo + hi) >> 1;
-          if (p.idx[mid] < key) lo = mid + 1;
-          else hi = mid;
-        }
-        const int64_t n = __shfl_down_sync(0xffffffffu, lo, 1) - lo;
+        const int64_t key = static_cast<int64_t>(blockIdx.x) * kBN;
+        const int64_t lo = warp_lower_bound(p.idx, rows, key, lane);
+        const int64_t n = warp_lower_bound(p.idx, rows, key + kBN < p.N ? key + kBN : p.N, lane) - lo;
         if (lane == 0) {
           s_row0 = static_cast<int>(lo);
           s_nrows = static_cast<int>(n < 0 ? 0 : (n > kBM ? kBM : n));
@@ -216,11 +218,18 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       mbar_init(bar(L::v_full + s), kConvThreads);
       mbar_init(bar(L::v_empty + s), 1);
     }
+    for (int s = 0; s < L::kCStages; ++s) {
+      mbar_init(bar(L::c_full + s), 1);
+      mbar_init(bar(L::c_empty + s), kConvThreads);
+    }
     mbar_init(bar(L::drain), 1);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) tmem_alloc<kTmemCols>(smem_u32(&s_tmem));
-  if (warp == kTmaWarp && lane == 0) tma_prefetch_desc(&tmK);
+  if (warp == kTmaWarp && lane == 0) {
+    tma_prefetch_desc(&tmK);
+    if (kOneSet) tma_prefetch_desc(&tmV);
+  }
   const int nkt = static_cast<int>((p.N + kBN - 1) / kBN);
   // split z covers the key tiles [kt0, kt0 + ntiles)
   const int kt0 = static_cast<int>((static_cast<int64_t>(nkt) * blockIdx.z) / prm.nsplit);
@@ -257,66 +266,106 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   auto key_tile = [&](int q) -> int { return masked ? sList[q] : kt0 + q; };
 
   auto tma_role = [&]() {
-    // ================================ K producer =======================================
-    if (lane == 0) {
-      int issued = 0;
+    // ================================ TMA producer =====================================
+    if (elect_one()) {
+      int issued_k = 0, issued_c = 0;
       for (int q = 0; q < ntiles; ++q) {
-        const int st = q % L::kKStages;
+        const int st = q % L::kKStages, key0 = key_tile(q) * kBN;
         if (q >= L::kKStages &&
             !mbar_wait(bar(L::k_empty + st), ((q / L::kKStages) - 1) & 1, &s_abort, prm.status))
           break;
         mbar_expect_tx(bar(L::k_full + st), L::kKTile);
-        tma_load_3d(sbase + L::kK + st * L::kKTile, &tmK, 0, h, key_tile(q) * kBN, bar(L::k_full + st));
-        issued = q + 1;
+        tma_load_3d(sbase + L::kK + st * L::kKTile, &tmK, 0, h, key0, bar(L::k_full + st));
+        issued_k = q + 1;
+        if constexpr (kOneSet) {
+          const int sc = q % L::kCStages;
+          if (q >= L::kCStages &&
+              !mbar_wait(bar(L::c_empty + sc), ((q / L::kCStages) - 1) & 1, &s_abort, prm.status))
+            break;
+          mbar_expect_tx(bar(L::c_full + sc), L::kKTile);
+          tma_load_3d(sbase + L::kC + sc * L::kKTile, &tmV, 0, h, key0, bar(L::c_full + sc));
+          issued_c = q + 1;
+        }
       }
       // every load issued above must land before the CTA may exit
-      for (int q = issued > L::kKStages ? issued - L::kKStages : 0; q < issued; ++q)
+      for (int q = issued_k > L::kKStages ? issued_k - L::kKStages : 0; q < issued_k; ++q)
         drain_wait(bar(L::k_full + q % L::kKStages), (q / L::kKStages) & 1);
+      if constexpr (kOneSet)
+        for (int q = issued_c > L::kCStages ? issued_c - L::kCStages : 0; q < issued_c; ++q)
+          drain_wait(bar(L::c_full + q % L::kCStages), (q / L::kCStages) & 1);
     }
+    __syncwarp();
   };
 
   auto conv_role = [&]() {
     // ================================ V converters ======================================
-    // kLanes threads hold a key's D codes (16 each); the codes of the next tile are loaded as
-    // those of this one leave the registers.
+    // kLanes threads hold a key's D codes (16 each), kRows keys at a time. The swizzle of a thread's chunks
+    // is the same in every pass (kRows is a multiple of 8): channels 16 l .. 16 l + 15 are the 16-byte chunks
+    // 2 l and 2 l + 1 of the f16 row; with D = 128 lanes 4-7 (second 64-channel sub-tile) store theirs in the
+    // other order, so 8 lanes cover all banks.
     constexpr int kLanes = D / 16;
     constexpr int kRows = kConvThreads / kLanes;   // keys of one pass
     constexpr int kPass = kBN / kRows;
+    static_assert(kRows % 8 == 0, "swizzle");
     const int ct = tid - kConvWarp * 32;
     const int l = ct % kLanes, r0 = ct / kLanes;
-    uint4 buf[kPass];
-    auto load = [&](int q, int i) {
-      const int64_t key = static_cast<int64_t>(key_tile(q)) * kBN + i * kRows + r0;
-      // keys past N become zeros (their P' is 0)
-      buf[i] = key < p.N ? __ldg(reinterpret_cast<const uint4*>(prm.v8 + (key * p.H + h) * D) + l)
-                         : make_uint4(0u, 0u, 0u, 0u);
+    const int odd = l >> 2, c0 = (2 * l) & 7;
+    const uint32_t row = (l / 4) * L::kSub + r0 * 128;
+    const uint32_t to_a = row + (((c0 + odd) ^ (r0 & 7)) << 4), to_b = row + (((c0 + 1 - odd) ^ (r0 & 7)) << 4);
+    auto convert = [&](uint8_t* tile, int i, uint4 w) {
+      const uint4 a = make_uint4(e4m3x2_to_f16x2(w.x), e4m3x2_to_f16x2(w.x >> 16), e4m3x2_to_f16x2(w.y),
+                                 e4m3x2_to_f16x2(w.y >> 16));
+      const uint4 b = make_uint4(e4m3x2_to_f16x2(w.z), e4m3x2_to_f16x2(w.z >> 16), e4m3x2_to_f16x2(w.w),
+                                 e4m3x2_to_f16x2(w.w >> 16));
+      *reinterpret_cast<uint4*>(tile + to_a + i * kRows * 128) = odd ? b : a;
+      *reinterpret_cast<uint4*>(tile + to_b + i * kRows * 128) = odd ? a : b;
     };
-    if (ntiles > 0)
+    auto wait_slot = [&](int q) -> bool {
+      return q < L::kVStages ||
+             mbar_wait(bar(L::v_empty + q % L::kVStages), ((q / L::kVStages) - 1) & 1, &s_abort, prm.status);
+    };
+    uint4 buf[kPass];
+    if constexpr (kOneSet) {
+      for (int q = 0; q < ntiles; ++q) {
+        const int st = q % L::kVStages, sc = q % L::kCStages;
+        if (!mbar_wait(bar(L::c_full + sc), (q / L::kCStages) & 1, &s_abort, prm.status)) break;
+        const uint4* codes = reinterpret_cast<const uint4*>(gbase + L::kC + sc * L::kKTile) + ct;
 #pragma unroll
-      for (int i = 0; i < kPass; ++i) load(0, i);
-    for (int q = 0; q < ntiles; ++q) {
-      const int st = q % L::kVStages;
-      if (q >= L::kVStages && !mbar_wait(bar(L::v_empty + st), ((q / L::kVStages) - 1) & 1, &s_abort, prm.status))
-        break;
-      uint8_t* tile = gbase + L::kV + st * L::kVTile;
+        for (int i = 0; i < kPass; ++i) buf[i] = codes[i * kConvThreads];
+        mbar_arrive(bar(L::c_empty + sc));
+        if (!wait_slot(q)) break;
 #pragma unroll
-      for (int i = 0; i < kPass; ++i) {
-        const int r = i * kRows + r0;
-        const uint4 w = buf[i];
-        if (q + 1 < ntiles) load(q + 1, i);
-        const uint4 a = make_uint4(e4m3x2_to_f16x2(w.x), e4m3x2_to_f16x2(w.x >> 16), e4m3x2_to_f16x2(w.y),
-                                   e4m3x2_to_f16x2(w.y >> 16));
-        const uint4 b = make_uint4(e4m3x2_to_f16x2(w.z), e4m3x2_to_f16x2(w.z >> 16), e4m3x2_to_f16x2(w.w),
-                                   e4m3x2_to_f16x2(w.w >> 16));
-        // channels 16 l .. 16 l + 15 = the 16-byte chunks 2l and 2l + 1; with D = 128 lanes 4-7 (second
-        // 64-channel sub-tile) store theirs in the other order, so 8 lanes cover all banks
-        uint8_t* row = tile + (l / 4) * L::kSub + r * 128;
-        const int c = (2 * l) & 7, odd = l >> 2;
-        *reinterpret_cast<uint4*>(row + (((c + odd) ^ (r & 7)) << 4)) = odd ? b : a;
-        *reinterpret_cast<uint4*>(row + (((c + 1 - odd) ^ (r & 7)) << 4)) = odd ? a : b;
+        for (int i = 0; i < kPass; ++i) convert(gbase + L::kV + st * L::kVTile, i, buf[i]);
+        fence_proxy_async_smem();
+        mbar_arrive(bar(L::v_full + st));
       }
-      fence_proxy_async_smem();
-      mbar_arrive(bar(L::v_full + st));
+    } else {
+      // the codes of the next tile are loaded as those of this one leave the registers
+      const int64_t step = static_cast<int64_t>(kRows) * p.H * D;
+      const uint8_t* mine = prm.v8 + (static_cast<int64_t>(r0) * p.H + h) * D + l * 16;
+      auto load = [&](const uint8_t* at, int q, int i) {
+        // keys past N become zeros (their P' is 0)
+        const bool in = static_cast<int64_t>(key_tile(q)) * kBN + i * kRows + r0 < p.N;
+        buf[i] = in ? __ldg(reinterpret_cast<const uint4*>(at + i * step)) : make_uint4(0u, 0u, 0u, 0u);
+      };
+      const int64_t tile_bytes = static_cast<int64_t>(kBN) * p.H * D;
+      if (ntiles > 0)
+#pragma unroll
+        for (int i = 0; i < kPass; ++i) load(mine + key_tile(0) * tile_bytes, 0, i);
+      for (int q = 0; q < ntiles; ++q) {
+        const int st = q % L::kVStages;
+        if (!wait_slot(q)) break;
+        const int qn = q + 1 < ntiles ? q + 1 : q;
+        const uint8_t* next = mine + key_tile(qn) * tile_bytes;
+#pragma unroll
+        for (int i = 0; i < kPass; ++i) {
+          const uint4 w = buf[i];
+          load(next, qn, i);
+          convert(gbase + L::kV + st * L::kVTile, i, w);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar(L::v_full + st));
+      }
     }
   };
 
@@ -664,14 +713,14 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 }
 
 // ---- host ------------------------------------------------------------------------------------
-// [N, H, d] e4m3 codes -> 3-D map (d, H, N), box (d, 1, 128): one swizzle row per key.
-int make_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, int64_t N, int H, int d) {
+// [N, H, d] e4m3 codes -> 3-D map (d, H, N), box (d, 1, 128): one row per key (K: one swizzle row).
+int make_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, int64_t N, int H, int d, CUtensorMapSwizzle swizzle) {
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(N)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H) * d};
   cuuint32_t box[3] = {static_cast<cuuint32_t>(d), 1, kBN};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
     return fail(TPS_ERR_CUDA, "pruned_attn_q8: cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
@@ -728,13 +777,13 @@ size_t ws_bytes_of(int split, int64_t cap, int H, int d) {
 }
 
 template <int D, bool kOneSet>
-int launch(const CUtensorMap& mk, const Q8Params& prm, cudaStream_t st) {
+int launch(const CUtensorMap& mk, const CUtensorMap& mv, const Q8Params& prm, cudaStream_t st) {
   constexpr int kSmem = Layout<D, kOneSet>::kAlloc;
   if (int e = smem_attribute<attn_q8_kernel<D, kOneSet>>(kSmem)) return e;
   const int per = kOneSet ? kBM : kTiles * kBM;
   const int64_t gx = prm.a.bm ? prm.a.nb : (prm.a.cap + per - 1) / per;
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(prm.a.H), static_cast<unsigned>(prm.nsplit));
-  attn_q8_kernel<D, kOneSet><<<grid, kThreads, kSmem, st>>>(mk, prm);
+  attn_q8_kernel<D, kOneSet><<<grid, kThreads, kSmem, st>>>(mk, mv, prm);
   return launch_status("pruned_attn_q8");
 }
 
@@ -776,8 +825,10 @@ extern "C" int pruned_attn_q8(const tps_bf16* q_act, const uint8_t* k_cache, con
   int err;
   prm.status = device_status(&err);
   if (!prm.status) return err;
-  CUtensorMap mk;
-  if (int e = make_map(enc, &mk, k_cache, N, H, d)) return e;
+  CUtensorMap mk, mv;
+  if (int e = make_map(enc, &mk, k_cache, N, H, d, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+    return e;
+  if (int e = make_map(enc, &mv, v_cache, N, H, d, CU_TENSOR_MAP_SWIZZLE_NONE)) return e;
   prm.v8 = v_cache;
   prm.ks = k_scale;
   prm.vs = v_scale;
@@ -790,8 +841,8 @@ extern "C" int pruned_attn_q8(const tps_bf16* q_act, const uint8_t* k_cache, con
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int e;
-  if (plan.one_set) e = d == 64 ? launch<64, true>(mk, prm, st) : launch<128, true>(mk, prm, st);
-  else e = d == 64 ? launch<64, false>(mk, prm, st) : launch<128, false>(mk, prm, st);
+  if (plan.one_set) e = d == 64 ? launch<64, true>(mk, mv, prm, st) : launch<128, true>(mk, mv, prm, st);
+  else e = d == 64 ? launch<64, false>(mk, mv, prm, st) : launch<128, false>(mk, mv, prm, st);
   if (!e && plan.split > 1)
     e = merge_split_parts(prm.o_part, prm.lse_part, plan.split, count, cap, H, d, o_act, lse, st);
   return e ? e : ok();
