@@ -75,11 +75,11 @@ struct Layout {
   static constexpr int kKTile = kBN * D;
   static constexpr int kSub = kBN * 128;                 // [128 keys x 64 f16], 128-byte swizzle
   static constexpr int kVTile = (D / 64) * kSub;
-  static constexpr int kQ = 0;                           // [tile][hi, lo]
-  static constexpr int kV = kQ + (kOneSet ? 1 : kTiles) * 2 * kQPart;
+  static constexpr int kV = 0;
   static constexpr int kK = kV + kVStages * kVTile;
   static constexpr int kC = kK + kKStages * kKTile;      // V's codes
-  static constexpr int kList = kC + kCStages * kKTile;   // uint16 kept key blocks (kOneSet)
+  static constexpr int kQ = kC + kCStages * kKTile;      // [tile][hi, lo]; not first: see the lane shift
+  static constexpr int kList = kQ + (kOneSet ? 1 : kTiles) * 2 * kQPart;   // uint16 kept key blocks (kOneSet)
   static constexpr int kBar = kList + (kOneSet ? 2 * kListMax : 0);
   static constexpr int kBytes = kBar + 512;
   static constexpr int kAlloc = kBytes + 1024;           // slack for 1024-byte alignment
@@ -199,6 +199,9 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   // active softmax warps of tile t: those with a row; the others have nothing to do
   const int rows_t0 = nrows < kBM ? nrows : kBM;
   const int rows_t1 = kOneSet ? rows_t0 : (nrows > kBM ? nrows - kBM : 0);
+  // One set of at most 64 rows: tile 1 holds them in lanes 64-127 (its A operand starts 64 rows before Q's;
+  // what lanes 0-63 then compute is not used), so that the two tiles' warps sit on different schedulers.
+  const int shift = kOneSet && nrows <= kBM / 2 ? kBM / 2 : 0;
   if (tid == 0) {
     s_abort = 0;
     for (int t = 0; t < kTiles; ++t) {
@@ -380,7 +383,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       const uint64_t dq = base(sbase + L::kQ), dk = base(sbase + L::kK);
       const uint64_t dv = sdesc_sw128(sbase + L::kV, L::kSub, 1024);
       auto issue_s = [&](int t, int u, int st) {
-        const uint64_t da = dq + ((kOneSet ? 0 : t) * 2 * L::kQPart >> 4);
+        const uint64_t da = kOneSet ? dq - (t == 1 ? shift * D >> 4 : 0) : dq + (t * 2 * L::kQPart >> 4);
         const uint64_t db = dk + ((st * L::kKTile + u * (L::kKTile / 2)) >> 4);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {     // hi parts, then lo parts, 32 channels each
@@ -442,7 +445,8 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   auto softmax_role = [&]() {
     // ================================ softmax warps ====================================
     const int t = warp >> 2;
-    const int r = (warp & 3) * 32 + lane;         // row of the tile == TMEM lane
+    const int off_lane = t == 1 ? shift : 0;
+    const int r = ((warp & 3) * 32 + lane - off_lane) & (kBM - 1);   // row of the tile, in TMEM lane r + off_lane
     const int lrow = (kOneSet ? 0 : t * kBM) + r;
     const bool valid = lrow < nrows;
     const int64_t row = row0 + lrow;
@@ -500,7 +504,8 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     const int nsteps = steps(t);
-    const bool works = (warp & 3) * 32 < (t ? rows_t1 : rows_t0) || (warp & 3) == 0;
+    const int first = ((warp & 3) * 32 - off_lane) & (kBM - 1);      // row of this warp's lane 0
+    const bool works = first < (t ? rows_t1 : rows_t0) || first == 0;
     auto scales = [&](int j, float& ks, float& vs) {
       const int64_t at = static_cast<int64_t>(key_tile(seq(t, j))) * p.H + h;
       ks = __ldg(prm.ks + at);
