@@ -31,8 +31,7 @@
 //   streams only the key tiles its query block keeps, so a block that is not kept is
 //   never read, whatever it holds.
 // Warps: 0-3 / 4-7 softmax of tile 0 / 1 (thread r = row r = TMEM lane r), 8-11 converters of V,
-// 12 TMA producer of K, 13 MMA issuer and TMEM owner, 14-15 idle (they complete the
-// warpgroup whose registers go to the softmax). Every mbarrier wait is bounded:
+// 12 TMA producer, 13 MMA issuer and TMEM owner, 14 MMA issuer of tile 1 (one set), the rest idle. Every mbarrier wait is bounded:
 // on expiry the CTA sets the device status word (TPS_ERR_TIMEOUT), drains what it
 // issued, frees TMEM and returns.
 #include "attn_common.cuh"
@@ -89,8 +88,9 @@ struct Layout {
   // is through with its second half arrive in the place of one that is still at its first.)
   static constexpr int s_full = q_full + kTiles;
   static constexpr int p_full = s_full + 2 * kTiles;
-  static constexpr int pv_done = p_full + 2 * kTiles;
-  static constexpr int k_full = pv_done + 2 * kTiles;    // + stage
+  static constexpr int o_part = p_full + 2 * kTiles;     // + tile: the last step's first half is in O_t
+  static constexpr int o_full = o_part + kTiles;         // + tile: all of O_t
+  static constexpr int k_full = o_full + kTiles;         // + stage
   static constexpr int k_empty = k_full + kKStages;
   static constexpr int v_full = k_empty + kKStages;
   static constexpr int v_empty = v_full + kVStages;
@@ -149,6 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                const __grid_constant__ Q8Params prm) {
   using L = Layout<D, kOneSet>;
+  constexpr int kIssuers = kOneSet ? kTiles : 1;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ int s_row0, s_nrows;
@@ -196,21 +197,25 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   uint16_t* sList = reinterpret_cast<uint16_t*>(gbase + L::kList);
 
   // ---- setup: barriers, TMEM, key tiles ---------------------------------------------------------
-  // active softmax warps of tile t: those with a row; the others have nothing to do
   const int rows_t0 = nrows < kBM ? nrows : kBM;
   const int rows_t1 = kOneSet ? rows_t0 : (nrows > kBM ? nrows - kBM : 0);
+  // Warp w of tile t (lanes 32 w .. 32 w + 31) works if it has a row; warp 0's row 0 always counts as one.
   // One set of at most 64 rows: tile 1 holds them in lanes 64-127 (its A operand starts 64 rows before Q's;
   // what lanes 0-63 then compute is not used), so that the two tiles' warps sit on different schedulers.
   const int shift = kOneSet && nrows <= kBM / 2 ? kBM / 2 : 0;
+  auto first_row = [&](int t, int w) { return (w * 32 - (t == 1 ? shift : 0)) & (kBM - 1); };
+  auto has_rows = [&](int t, int w) { return first_row(t, w) < (t ? rows_t1 : rows_t0) || first_row(t, w) == 0; };
   if (tid == 0) {
     s_abort = 0;
     for (int t = 0; t < kTiles; ++t) {
-      const int w = ((t ? rows_t1 : rows_t0) + 31) / 32;
       mbar_init(bar(L::q_full + t), kOneSet ? kSoftmaxThreads : kBM);
+      mbar_init(bar(L::o_part + t), 1);
+      mbar_init(bar(L::o_full + t), 1);
+      int warps = 0;                // that store P'_t
+      for (int w = 0; w < 4; ++w) warps += has_rows(t, w) ? 1 : 0;
       for (int u = 0; u < 2; ++u) {
         mbar_init(bar(L::s_full + 2 * t + u), 1);
-        mbar_init(bar(L::p_full + 2 * t + u), 32 * (w > 0 ? w : 1));
-        mbar_init(bar(L::pv_done + 2 * t + u), 1);
+        mbar_init(bar(L::p_full + 2 * t + u), 32 * warps);
       }
     }
     for (int s = 0; s < L::kKStages; ++s) {
@@ -225,7 +230,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       mbar_init(bar(L::c_full + s), 1);
       mbar_init(bar(L::c_empty + s), kConvThreads);
     }
-    mbar_init(bar(L::drain), 1);
+    mbar_init(bar(L::drain), kIssuers);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) tmem_alloc<kTmemCols>(smem_u32(&s_tmem));
@@ -372,10 +377,16 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     }
   };
 
-  auto mma_role = [&]() {
+  auto mma_role = [&](int me) {
     // ================================ MMA issuer =======================================
-    // One thread issues every MMA, so the cycles between two issues count: descriptors are a base
-    // plus a constant in the 14-bit address field (shared memory ends below 2^18 bytes: no carry).
+    // One thread issues the MMAs of both tiles, in turns, or (one set) each tile has its own. The tensor
+    // pipe queues 8 MMAs, about 400 clocks of work, and a commit, a wait that finds its barrier ready and a
+    // tcgen05 fence cost the issuer 50-200 clocks each, so a single one leaves the pipe waiting: with two,
+    // one token over the HSA cache took 154 us instead of 179. With shared key tiles two issuers lose: the
+    // tiles fall into step and both softmaxes wait for MMAs at once (middle video 656 us instead of 622).
+    // Descriptors are a base plus a constant in the 14-bit address field (shared memory ends
+    // below 2^18 bytes: no carry).
+    const int t_lo = kOneSet ? me : 0, t_hi = kOneSet ? me + 1 : kTiles;
     if (elect_one()) {
       constexpr uint32_t kIdescS = idesc_fmt0(kBM, kBN / 2, false, false);  // e4m3: Q (hi, lo) K^T, both K-major
       constexpr uint32_t kIdescO = idesc_fmt0(kBM, D, false, true);         // f16: P' V, V is MN-major
@@ -391,14 +402,13 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
           mma_f8_ss(tS(t, u), da + ((part * L::kQPart + kk * 32) >> 4), db + (kk * 32 >> 4), kIdescS, i > 0 ? 1u : 0u);
         }
         mma_commit(bar(L::s_full + 2 * t + u));
-        if (u == 1 && (kOneSet || t == kTiles - 1)) mma_commit(bar(L::k_empty + st));   // last reader of this stage
+        if (u == 1 && (kOneSet || t == kTiles - 1)) mma_commit(bar(L::k_empty + st));   // last reader
       };
       auto issue_o = [&](int t, int u, int st, bool first) {
         const uint64_t db = dv + ((st * L::kVTile + u * 64 * 128) >> 4);
 #pragma unroll
         for (int kk = 0; kk < kBN / 32; ++kk)
           mma_f16_ts(tO(t), tS(t, u) + 8 * kk, db + (kk * 16 * 128 >> 4), kIdescO, (u > 0 || kk > 0 || !first) ? 1u : 0u);
-        mma_commit(bar(L::pv_done + 2 * t + u));
         if (u == 1 && (kOneSet || t == kTiles - 1)) mma_commit(bar(L::v_empty + st));
       };
       auto wait_k = [&](int q) -> bool {
@@ -408,8 +418,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         return mbar_wait(bar(L::v_full + q % L::kVStages), (q / L::kVStages) & 1, &s_abort, prm.status);
       };
       bool ok = true;
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
+      for (int t = t_lo; t < t_hi; ++t) {
         if (!ok || steps(t) == 0) continue;
         ok = mbar_wait(bar(L::q_full + (kOneSet ? 0 : t)), 0, &s_abort, prm.status) && wait_k(seq(t, 0));
         tc_fence_after();
@@ -417,23 +426,24 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         issue_s(t, 0, seq(t, 0) % L::kKStages);
         issue_s(t, 1, seq(t, 0) % L::kKStages);
       }
-      // Step j: for each half and tile O_t += P'_t V, and S_t of that half of the next key tile in its place
-      // (it overwrites the columns P'_t was read from: MMAs of one thread run in issue order). While a
-      // softmax warp is at one half, the MMAs of its other half run.
-      for (int j = 0; ok && j < steps(0); ++j) {
+      // Step j: for each half O_t += P'_t V, and S_t of that half of the next key tile in its place (it overwrites
+      // the columns P'_t was read from: MMAs of one thread run in issue order). While a softmax warp is at one
+      // half, the MMAs of its other half run.
+      const int n = steps(t_lo);
+      for (int j = 0; ok && j < n; ++j) {
+        const int q = seq(t_lo, j), qn = seq(t_lo, j + 1);
+        const bool more = j + 1 < n;
+        ok = wait_v(q) && (!more || wait_k(qn));
+        const int sv = q % L::kVStages, sk = qn % L::kKStages;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-#pragma unroll
-          for (int t = 0; t < kTiles; ++t) {
-            if (!ok || j >= steps(t)) continue;
-            const int q = seq(t, j), qn = seq(t, j + 1);
-            const bool more = j + 1 < steps(t);
-            if (u == 0 && (kOneSet || t == 0)) ok = wait_v(q) && (!more || wait_k(qn));
-            ok = ok && mbar_spin(bar(L::p_full + 2 * t + u), j & 1, &s_abort, prm.status);
-            if (!ok) continue;
+          for (int t = t_lo; t < t_hi; ++t) {
+            ok = ok && mbar_wait(bar(L::p_full + 2 * t + u), j & 1, &s_abort, prm.status);
+            if (!ok) break;
             tc_fence_after();
-            issue_o(t, u, q % L::kVStages, j == 0);
-            if (more) issue_s(t, u, qn % L::kKStages);
+            issue_o(t, u, sv, j == 0);
+            if (more) issue_s(t, u, sk);
+            else mma_commit(bar((u == 0 ? L::o_part : L::o_full) + t));
           }
         }
       }
@@ -504,8 +514,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     const int nsteps = steps(t);
-    const int first = ((warp & 3) * 32 - off_lane) & (kBM - 1);      // row of this warp's lane 0
-    const bool works = first < (t ? rows_t1 : rows_t0) || first == 0;
+    const bool works = has_rows(t, warp & 3);
     auto scales = [&](int j, float& ks, float& vs) {
       const int64_t at = static_cast<int64_t>(key_tile(seq(t, j))) * p.H + h;
       ks = __ldg(prm.ks + at);
@@ -576,10 +585,12 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
           if (j == 0 && u == 0) {
             m_run = m_new;
           } else if (__any_sync(0xffffffffu, m_new > m_run)) {
-            // O, complete up to the half before, is rescaled
+            // O, complete up to the half before, is rescaled. The MMAs of that half are followed by those of the
+            // next S in its columns (or, in the last step, by a commit of their own).
             const float alpha = fast_exp2(m_run - m_new);
-            if (!__all_sync(0xffffffffu, mbar_wait(bar(L::pv_done + 2 * t + 1 - u), (j - 1 + u) & 1, &s_abort, prm.status)))
-              ok = false;
+            const bool last = u == 1 && j + 1 == nsteps;
+            const uint32_t before = last ? bar(L::o_part + t) : bar(L::s_full + 2 * t + 1 - u);
+            if (!__all_sync(0xffffffffu, mbar_wait(before, last ? 0 : (j + u) & 1, &s_abort, prm.status))) ok = false;
             tc_fence_after();
 #pragma unroll
             for (int i0 = 0; i0 < D; i0 += 16) {    // few registers: sr is held meanwhile
@@ -608,7 +619,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       if (!ok) break;
     }
     // ---- epilogue ------------------------------------------------------------------------
-    if (ok && nsteps > 0) ok = mbar_wait(bar(L::pv_done + 2 * t + 1), (nsteps - 1) & 1, &s_abort, prm.status);
+    if (ok && nsteps > 0) ok = mbar_wait(bar(L::o_full + t), 0, &s_abort, prm.status);
     ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
     float w0 = 1.f, w1 = 0.f;                     // weights of this tile's and the other tile's sums
@@ -704,7 +715,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   if (warp >= kTmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
     if (warp == kTmaWarp) tma_role();
-    else if (warp == kMmaWarp) mma_role();
+    else if (warp >= kMmaWarp && warp < kMmaWarp + kIssuers) mma_role(warp - kMmaWarp);
     tail();
   } else if (warp >= kConvWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));

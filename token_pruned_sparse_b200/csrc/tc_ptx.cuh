@@ -73,22 +73,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   return mbar_wait_for(bar, parity, abort_flag, status, kWaitLimitCycles);
 }
 
-// mbar_wait that first polls without suspending the thread (mbarrier.test_wait): for the one
-// thread whose wake-up delay every other warp waits for.
-__device__ __forceinline__ bool mbar_spin(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                          unsigned int* status) {
-  for (int i = 0; i < 256; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (ok) return true;
-  }
-  return mbar_wait(bar, parity, abort_flag, status);
-}
-
 // Teardown wait: bounded, ignores the abort flag (used to drain work this
 // thread issued before the CTA exits).
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
