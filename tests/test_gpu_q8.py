@@ -287,6 +287,44 @@ def test_attn_q8_dense(N, A, H, d, sharp):
     _check_attn(o, lse, cache, q, idx, scale)
 
 
+@pytest.mark.parametrize("N,A,H,d", [(1, 1, 3, 64), (15, 8, 2, 128), (129, 9, 2, 64), (300, 16, 2, 128), (1000, 2, 24, 128),
+                                     (5003, 16, 3, 64), (9001, 9, 2, 128), (20280, 1, 12, 128), (2049, 3, 128, 64)])
+@pytest.mark.parametrize("sharp", [False, True])
+def test_attn_q8_few_rows(N, A, H, d, sharp):
+    cache, q, idx = _attn_case(N, A, H, d, N + A)
+    scale = 0.35 if sharp else 1.0 / math.sqrt(d)
+    o, lse = _run_attn(cache, q, idx, scale, room=3)
+    _check_attn(o, lse, cache, q, idx, scale)
+    none = torch.empty(0, dtype=torch.uint8, device=DEV)
+    o1, _ = _run_attn(cache, q, idx, scale, ws=none, lse=False)       # one key range per head
+    _check_attn(o1, None, cache, q, idx, scale)
+
+
+def test_attn_q8_full_waves_then_a_split_tail():
+    """More row tiles than one wave of this GPU holds: the last ones go in a second, split launch."""
+    N, A, H, d = 2100, 2000, 24, 64
+    cache, q, idx = _attn_case(N, A, H, d, 3)
+    scale = 1.0 / math.sqrt(d)
+    o, lse = _run_attn(cache, q, idx, scale, room=5)
+    _check_attn(o, lse, cache, q, idx, scale)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("A", [3, 16, 60, 128, 300])
+@pytest.mark.parametrize("where", [[0], [1], [17], list(range(0, 20, 2)), list(range(1, 20, 2)), list(range(20))])
+def test_attn_q8_nan_keys_reach_every_row(d, A, where):
+    """A key block whose codes are all NaN makes every attending row NaN, whichever key range, stream or warp sees
+    it and even where that part sees nothing else."""
+    N, H = 20 * 128 - 5, 1
+    cache, q, idx = _attn_case(N, A, H, d, 41)
+    dev = list(_to_dev(cache))
+    for b in where:
+        dev[0][b * 128:(b + 1) * 128] = 0x7F
+    for ws in (None, torch.empty(0, dtype=torch.uint8, device=DEV)):
+        o, lse = _run_attn(cache, q, idx, 1.0 / math.sqrt(d), dev=dev, ws=ws)
+        assert np.isnan(o).all() and np.isnan(lse).all()
+
+
 @pytest.mark.parametrize("N,A,H,d", [(6000, 33, 5, 128), (4099, 700, 2, 64)])
 def test_attn_q8_without_workspace_and_without_lse(N, A, H, d):
     cache, q, idx = _attn_case(N, A, H, d, 5)
@@ -336,9 +374,10 @@ def test_attn_q8_nan_only_where_it_is_attended(d):
 
 
 @pytest.mark.parametrize("d", [64, 128])
-def test_attn_q8_rising_maxima_force_rescales(d):
+@pytest.mark.parametrize("A", [200, 100, 11])
+def test_attn_q8_rising_maxima_force_rescales(d, A):
     """Keys that grow along the cache: the running maximum moves again and again, far beyond what f16 holds."""
-    N, A, H = 1500, 200, 1
+    N, H = 1500, 1
     rng = np.random.default_rng(3)
     u = rng.standard_normal(d)
     grow = np.linspace(0.1, 12.0, N)[:, None, None]
@@ -354,8 +393,9 @@ def test_attn_q8_rising_maxima_force_rescales(d):
 
 
 @pytest.mark.parametrize("d", [64, 128])
-def test_attn_q8_scales_zero_far_apart_and_any_number(d):
-    N, A, H = 700, 150, 2
+@pytest.mark.parametrize("A", [150, 40, 5])
+def test_attn_q8_scales_zero_far_apart_and_any_number(d, A):
+    N, H = 700, 2
     cache, q, idx = _attn_case(N, A, H, d, 31)
     (kv, ks), (vv, vs) = cache
     ks, vs = ks.copy(), vs.copy()

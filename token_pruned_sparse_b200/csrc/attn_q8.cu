@@ -34,7 +34,7 @@
 // 12 TMA producer, 13 MMA issuer and TMEM owner, 14 MMA issuer of tile 1 (one set), the rest idle. Every mbarrier wait is bounded:
 // on expiry the CTA sets the device status word (TPS_ERR_TIMEOUT), drains what it
 // issued, frees TMEM and returns.
-#include "attn_common.cuh"
+#include "attn_q8.cuh"
 #include "q8.cuh"
 #include "tc_ptx.cuh"
 #include "tma_host.cuh"
@@ -103,18 +103,6 @@ struct Layout {
   static_assert(!kOneSet || kVStages * kVTile + kKStages * kKTile >= kBM * D * 4, "merge staging");
 };
 
-struct Q8Params {
-  AttnArgs a;          // a.k / a.v are not used
-  const uint8_t* v8;
-  const float* ks;
-  const float* vs;
-  float scale_log2;
-  int nsplit;          // key-range splits (blockIdx.z)
-  float* o_part;       // nsplit > 1: normalised fp32 partials [nsplit][cap][H][D] and their
-  float* lse_part;     // log-sum-exp [nsplit][cap][H]
-  unsigned int* status;
-};
-
 __device__ __forceinline__ void barrier_all() { asm volatile("barrier.sync 0;" ::: "memory"); }
 __device__ __forceinline__ void barrier_softmax() {
   asm volatile("barrier.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
@@ -147,7 +135,7 @@ __device__ __forceinline__ void exp_cols_f16(const uint32_t (&sr)[32], uint64_t 
 template <int D, bool kOneSet>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-               const __grid_constant__ Q8Params prm) {
+               const __grid_constant__ Q8Args prm) {
   using L = Layout<D, kOneSet>;
   constexpr int kIssuers = kOneSet ? kTiles : 1;
   extern __shared__ uint8_t smem_raw[];
@@ -164,7 +152,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   const bool masked = kOneSet && p.bm != nullptr;
 
   // ---- this CTA's rows: [row0, row0 + nrows) of the compacted queries -----------------------
-  int64_t row0 = static_cast<int64_t>(blockIdx.x) * (kOneSet ? kBM : kTiles * kBM);
+  int64_t row0 = (static_cast<int64_t>(blockIdx.x) + prm.tile0) * (kOneSet ? kBM : kTiles * kBM);
   int nrows = static_cast<int>(rows - row0 < kTiles * kBM ? rows - row0 : kTiles * kBM);
   if constexpr (kOneSet) {
     if (masked) {
@@ -523,9 +511,8 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     float ks_next = 0.f, vs_next = 0.f;
     if (works && nsteps > 0) scales(0, ks_next, vs_next);
     for (int j = 0; works && j < nsteps; ++j) {
-      // a scale of 0 (an empty block) stands for values of 0: the smallest positive factors give just that
-      const float c = fmaxf(rowc * ks_next, 1.17549435e-38f);
-      const float vs = fminf(fmaxf(vs_next, 7.8886091e-31f), 1.2676506e30f);   // 2^-100 .. 2^100
+      const float c = fmaxf(rowc * ks_next, kFactorMin);
+      const float vs = fminf(fmaxf(vs_next, kScaleMin), kScaleMax);
       const float lv = __log2f(vs), ivs = 1.f / vs;
       if (j + 1 < nsteps) scales(j + 1, ks_next, vs_next);
       const int64_t key0 = static_cast<int64_t>(key_tile(seq(t, j))) * kBN;
@@ -650,9 +637,9 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       ok = __all_sync(0xffffffffu, ok);
       const float2 ml = s_ml[r];
       const float m = fmaxf(m_run, ml.x);
-      w0 = m_run == -INFINITY ? 0.f : fast_exp2(m_run - m);
-      w1 = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m);
-      l_run = w0 * l_run + (w1 > 0.f ? w1 * ml.y : 0.f);
+      w0 = part_weight(m_run, l_run, m);
+      w1 = part_weight(ml.x, ml.y, m);
+      l_run = w0 * l_run + (w1 != 0.f ? w1 * ml.y : 0.f);
       m_run = m;
       other = reinterpret_cast<const float*>(stage);
     }
@@ -663,7 +650,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     w1 *= inv;
     const float lse = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
     const int64_t orow = row * p.H + h;
-    const int64_t prow = prm.nsplit > 1 ? static_cast<int64_t>(blockIdx.z) * p.cap * p.H + orow : 0;
+    const int64_t prow = prm.nsplit > 1 ? static_cast<int64_t>(blockIdx.z) * prm.part_rows * p.H + orow - prm.part_row0 * p.H : 0;
 #pragma unroll
     for (int i0 = 0; i0 < D; i0 += 32) {
       float o[32];
@@ -757,57 +744,122 @@ int smem_attribute(int bytes) {
   return TPS_OK;
 }
 
-// How a call runs: the row layout and the key-range split S of a dense call. Cost model in key-tile
-// steps: ceil(units S / SMs) waves of (steps / S + kEnds), kEnds = prologue and epilogue; a split
-// also pays the merge launch. Masked calls are one CTA per query block and head.
+// How a call runs. A unit of work is one row tile (256 rows, or one set of 128) of one head; U units on P SMs
+// take ceil(U / P) unit times. Two ways out of a mostly empty last wave: all units split S ways along the
+// keys, or the units of the full waves whole and the remaining tiles split S_t ways in a second launch.
+// Costs in steps of key tiles: a CTA of n steps takes n + kEnds (prologue and epilogue); a split pays
+// the merge launch, and the merge's traffic grows with S, so a plan must gain 2% on the one before it.
+// Masked calls are one CTA per query block and head.
 struct Plan {
+  bool few;             // the kernel of attn_q8_few.cu
   bool one_set;
-  int split;
+  int split;            // of the launch that has all tiles (main_tiles = 0), or of the tail
+  int64_t main_tiles;   // tiles of an unsplit first launch; 0: none
 };
 constexpr double kEnds = 6.0, kMerge = 3.0;
 constexpr int kMaxSplit = 32;
 
 Plan make_plan(int64_t cap, int64_t N, int H, bool masked) {
-  Plan best{masked || cap <= kBM, 1};
+  Plan best{!masked && cap <= kFewRows, masked || cap <= kBM, 1, 0};
   if (masked || cap < 1) return best;
-  const int64_t units = (best.one_set ? 1 : (cap + kTiles * kBM - 1) / (kTiles * kBM)) * H;
+  if (best.few) {
+    best.split = few_split(N, H);
+    return best;
+  }
+  const int64_t tiles = best.one_set ? 1 : (cap + kTiles * kBM - 1) / (kTiles * kBM);
+  const int64_t units = tiles * H;
   const int64_t nkt = (N + kBN - 1) / kBN;
   const double steps = best.one_set ? nkt / 2.0 : static_cast<double>(nkt);
   const int64_t P = sm_count();
+  auto cost_of = [&](int64_t u, int s) {
+    return static_cast<double>((u * s + P - 1) / P) * (steps / s + kEnds) + (s > 1 ? kMerge : 0.0);
+  };
   double cost = 1e300;
-  for (int s = 1; s <= kMaxSplit && (s == 1 || nkt >= 8 * s); ++s) {
-    const double waves = static_cast<double>((units * s + P - 1) / P);
-    const double c = waves * (steps / s + kEnds) + (s > 1 ? kMerge : 0.0);
-    if (c < 0.98 * cost) {
+  for (int s = 1; s <= kMaxSplit && (s == 1 || nkt >= 8 * s); ++s)
+    if (const double c = cost_of(units, s); c < 0.98 * cost) {
       cost = c;
       best.split = s;
     }
-  }
+  const int64_t whole = units / P * P / H;          // tiles that fit the full waves
+  if (whole >= 1 && whole < tiles)
+    for (int s = 2; s <= kMaxSplit && nkt >= 8 * s; ++s)
+      if (const double c = cost_of(whole * H, 1) + cost_of((tiles - whole) * H, s); c < 0.98 * cost) {
+        cost = c;
+        best.split = s;
+        best.main_tiles = whole;
+      }
   return best;
 }
 
-size_t ws_bytes_of(int split, int64_t cap, int H, int d) {
-  if (split <= 1) return 0;
-  const size_t o = static_cast<size_t>(split) * cap * H * d * sizeof(float);
-  return (o + 255) / 256 * 256 + static_cast<size_t>(split) * cap * H * sizeof(float);
+int64_t part_rows_of(const Plan& plan, int64_t cap) { return cap - plan.main_tiles * (kTiles * kBM); }
+
+size_t ws_bytes_of(const Plan& plan, int64_t cap, int H, int d) {
+  if (plan.split <= 1) return 0;
+  const size_t rows = static_cast<size_t>(plan.split) * part_rows_of(plan, cap) * H;
+  return (rows * d * sizeof(float) + 255) / 256 * 256 + rows * sizeof(float);
+}
+
+// The S-way merge of the partials: o = sum_s w_s o_s / sum_s w_s with w_s = exp(lse_s - max). A quarter-row of
+// 16-byte loads per thread; S loads in flight.
+template <int D>
+__global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Q8Args prm) {
+  const AttnArgs& p = prm.a;
+  const int64_t rows = active_count(p.count, p.cap) - prm.part_row0;
+  const int64_t plane = prm.part_rows * p.H;
+  const int64_t total = rows * p.H * (D / 4);
+  const float4* op = reinterpret_cast<const float4*>(prm.o_part);
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int64_t rh = i / (D / 4);
+    float m = -INFINITY, nan = 0.f;
+    for (int s = 0; s < prm.nsplit; ++s) {
+      const float l = prm.lse_part[s * plane + rh];
+      if (l != l) nan = l;
+      m = fmaxf(m, l);
+    }
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll 4
+    for (int s = 0; s < prm.nsplit; ++s) {
+      const float4 x = op[s * plane * (D / 4) + i];
+      const float w = expf(prm.lse_part[s * plane + rh] - ref);
+      if (w == 0.f) continue;
+      a.x = fmaf(w, x.x, a.x);
+      a.y = fmaf(w, x.y, a.y);
+      a.z = fmaf(w, x.z, a.z);
+      a.w = fmaf(w, x.w, a.w);
+      sum += w;
+    }
+    sum += nan;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int64_t orow = prm.part_row0 * p.H + rh;
+    reinterpret_cast<uint2*>(p.o + orow * D)[i % (D / 4)] =
+        make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+    if (p.lse && i % (D / 4) == 0) p.lse[orow] = sum == 0.f ? -INFINITY : ref + logf(sum);
+  }
+}
+
+int launch_merge(const Q8Args& prm, cudaStream_t st) {
+  const int64_t threads = prm.part_rows * prm.a.H * (prm.a.d / 4);
+  int64_t grid = (threads + 127) / 128;
+  const int64_t most = static_cast<int64_t>(sm_count()) * 16;
+  grid = grid < most ? grid : most;
+  if (prm.a.d == 128) merge_kernel<128><<<static_cast<unsigned>(grid), 128, 0, st>>>(prm);
+  else merge_kernel<64><<<static_cast<unsigned>(grid), 128, 0, st>>>(prm);
+  return launch_status("pruned_attn_q8: merge");
 }
 
 template <int D, bool kOneSet>
-int launch(const CUtensorMap& mk, const CUtensorMap& mv, const Q8Params& prm, cudaStream_t st) {
+int launch(const CUtensorMap& mk, const CUtensorMap& mv, const Q8Args& prm, int64_t tiles, cudaStream_t st) {
   constexpr int kSmem = Layout<D, kOneSet>::kAlloc;
   if (int e = smem_attribute<attn_q8_kernel<D, kOneSet>>(kSmem)) return e;
-  const int per = kOneSet ? kBM : kTiles * kBM;
-  const int64_t gx = prm.a.bm ? prm.a.nb : (prm.a.cap + per - 1) / per;
-  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(prm.a.H), static_cast<unsigned>(prm.nsplit));
+  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(prm.a.H), static_cast<unsigned>(prm.nsplit));
   attn_q8_kernel<D, kOneSet><<<grid, kThreads, kSmem, st>>>(mk, mv, prm);
   return launch_status("pruned_attn_q8");
 }
 
 }  // namespace
-
-// S-way merge of the split partials (merge.cu).
-int merge_split_parts(const float* o_part, const float* lse_part, int nsplit, const int32_t* count, int64_t cap,
-                      int H, int d, uint16_t* o, float* lse, cudaStream_t st);
 
 }  // namespace tps
 
@@ -816,7 +868,7 @@ extern "C" size_t tps_attn_q8_workspace_size(int64_t cap, int64_t N, int H, int 
   if (cap <= 0 || cap >= (INT64_C(1) << 31) || N <= 0 || N >= (INT64_C(1) << 31) || H <= 0 || H > 256 ||
       (d != 64 && d != 128))
     return 0;
-  return ws_bytes_of(make_plan(cap, N, H, false).split, cap, H, d);
+  return ws_bytes_of(make_plan(cap, N, H, false), cap, H, d);
 }
 
 extern "C" int pruned_attn_q8(const tps_bf16* q_act, const uint8_t* k_cache, const uint8_t* v_cache,
@@ -825,7 +877,7 @@ extern "C" int pruned_attn_q8(const tps_bf16* q_act, const uint8_t* k_cache, con
                               tps_bf16* o_act, float* lse, void* ws, size_t ws_bytes, tps_stream stream) {
   TPS_TRACE("pruned_attn_q8");
   using namespace tps;
-  Q8Params prm{};
+  Q8Args prm{};
   if (int e = attn_validate("pruned_attn_q8", q_act, reinterpret_cast<const tps_bf16*>(k_cache),
                             reinterpret_cast<const tps_bf16*>(v_cache), idx, count, cap, N, H, d, scale, blockmask,
                             block, o_act, lse, &prm.a))
@@ -835,31 +887,54 @@ extern "C" int pruned_attn_q8(const tps_bf16* q_act, const uint8_t* k_cache, con
     return fail(TPS_ERR_ALIGN, "pruned_attn_q8: scales and lse must be 4-byte aligned");
   if (cap == 0) return ok();
   Plan plan = make_plan(cap, N, H, blockmask != nullptr);
-  if (!ws || !aligned16(ws) || ws_bytes < ws_bytes_of(plan.split, cap, H, d)) plan.split = 1;
-  EncodeTiledFn enc;
-  if (int e = tensor_map_encoder(&enc, "pruned_attn_q8")) return e;
+  if (!ws || !aligned16(ws) || ws_bytes < ws_bytes_of(plan, cap, H, d)) {
+    plan.split = 1;
+    plan.main_tiles = 0;
+  }
   int err;
   prm.status = device_status(&err);
   if (!prm.status) return err;
-  CUtensorMap mk, mv;
-  if (int e = make_map(enc, &mk, k_cache, N, H, d, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
-    return e;
-  if (int e = make_map(enc, &mv, v_cache, N, H, d, CU_TENSOR_MAP_SWIZZLE_NONE)) return e;
   prm.v8 = v_cache;
   prm.ks = k_scale;
   prm.vs = v_scale;
   prm.scale_log2 = scale * kLog2e;
   prm.nsplit = plan.split;
   if (plan.split > 1) {
+    prm.part_row0 = plan.main_tiles * (kTiles * kBM);
+    prm.part_rows = part_rows_of(plan, cap);
     prm.o_part = static_cast<float*>(ws);
-    prm.lse_part = reinterpret_cast<float*>(
-        static_cast<char*>(ws) + (static_cast<size_t>(plan.split) * cap * H * d * sizeof(float) + 255) / 256 * 256);
+    prm.lse_part = reinterpret_cast<float*>(static_cast<char*>(ws) +
+                                            (static_cast<size_t>(plan.split) * prm.part_rows * H * d * sizeof(float) + 255) / 256 * 256);
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int e;
-  if (plan.one_set) e = d == 64 ? launch<64, true>(mk, mv, prm, st) : launch<128, true>(mk, mv, prm, st);
-  else e = d == 64 ? launch<64, false>(mk, mv, prm, st) : launch<128, false>(mk, mv, prm, st);
-  if (!e && plan.split > 1)
-    e = merge_split_parts(prm.o_part, prm.lse_part, plan.split, count, cap, H, d, o_act, lse, st);
+  if (plan.few) {
+    e = launch_attn_q8_few(prm, st);
+  } else {
+    EncodeTiledFn enc;
+    if (int r = tensor_map_encoder(&enc, "pruned_attn_q8")) return r;
+    CUtensorMap mk, mv;
+    if (int r = make_map(enc, &mk, k_cache, N, H, d, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+      return r;
+    if (int r = make_map(enc, &mv, v_cache, N, H, d, CU_TENSOR_MAP_SWIZZLE_NONE)) return r;
+    if (plan.one_set) {
+      const int64_t tiles = blockmask ? prm.a.nb : 1;
+      e = d == 64 ? launch<64, true>(mk, mv, prm, tiles, st) : launch<128, true>(mk, mv, prm, tiles, st);
+    } else {
+      const int64_t tiles = (cap + kTiles * kBM - 1) / (kTiles * kBM);
+      auto run = [&](const Q8Args& a, int64_t n) {
+        return d == 64 ? launch<64, false>(mk, mv, a, n, st) : launch<128, false>(mk, mv, a, n, st);
+      };
+      e = TPS_OK;
+      if (plan.main_tiles) {
+        Q8Args whole = prm;
+        whole.nsplit = 1;
+        e = run(whole, plan.main_tiles);
+        prm.tile0 = static_cast<int>(plan.main_tiles);
+      }
+      if (!e) e = run(prm, tiles - plan.main_tiles);
+    }
+  }
+  if (!e && plan.split > 1) e = launch_merge(prm, st);
   return e ? e : ok();
 }
