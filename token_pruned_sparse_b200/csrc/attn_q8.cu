@@ -803,6 +803,7 @@ size_t ws_bytes_of(const Plan& plan, int64_t cap, int H, int d) {
 // 16-byte loads per thread; S loads in flight.
 template <int D>
 __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Q8Args prm) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // launched ahead of the partials' end
   const AttnArgs& p = prm.a;
   const int64_t rows = active_count(p.count, p.cap) - prm.part_row0;
   const int64_t plane = prm.part_rows * p.H;
@@ -812,6 +813,7 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Q8Ar
        i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
     const int64_t rh = i / (D / 4);
     float m = -INFINITY, nan = 0.f;
+#pragma unroll 8
     for (int s = 0; s < prm.nsplit; ++s) {
       const float l = prm.lse_part[s * plane + rh];
       if (l != l) nan = l;
@@ -820,11 +822,10 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Q8Ar
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
     const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll 4
+#pragma unroll 8
     for (int s = 0; s < prm.nsplit; ++s) {
-      const float4 x = op[s * plane * (D / 4) + i];
+      const float4 x = op[s * plane * (D / 4) + i];       // (zeros where a part has no key)
       const float w = expf(prm.lse_part[s * plane + rh] - ref);
-      if (w == 0.f) continue;
       a.x = fmaf(w, x.x, a.x);
       a.y = fmaf(w, x.y, a.y);
       a.z = fmaf(w, x.z, a.z);
@@ -845,8 +846,19 @@ int launch_merge(const Q8Args& prm, cudaStream_t st) {
   int64_t grid = (threads + 127) / 128;
   const int64_t most = static_cast<int64_t>(sm_count()) * 16;
   grid = grid < most ? grid : most;
-  if (prm.a.d == 128) merge_kernel<128><<<static_cast<unsigned>(grid), 128, 0, st>>>(prm);
-  else merge_kernel<64><<<static_cast<unsigned>(grid), 128, 0, st>>>(prm);
+  // the launch itself overlaps the kernels of the partials; the merge kernel waits for their end
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = prm.a.d == 128 ? cudaLaunchKernelEx(&cfg, merge_kernel<128>, prm)
+                                       : cudaLaunchKernelEx(&cfg, merge_kernel<64>, prm);
+  if (e != cudaSuccess) return cuda_status(e, "pruned_attn_q8: merge launch");
   return launch_status("pruned_attn_q8: merge");
 }
 
