@@ -56,7 +56,7 @@ constexpr int kConvWarp = kSoftmaxThreads / 32;
 constexpr int kTmaWarp = kConvWarp + kConvThreads / 32;
 constexpr int kMmaWarp = kTmaWarp + 1;
 // 16 warps launch with 128 registers per thread; the warpgroups re-divide them
-constexpr int kLaunchRegs = 128, kSoftmaxRegs = 152, kConvRegs = 96, kProducerRegs = 112;
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 144, kConvRegs = 104, kProducerRegs = 120;
 static_assert(8 * kSoftmaxRegs + 4 * kConvRegs + 4 * kProducerRegs <= 16 * kLaunchRegs, "register split");
 constexpr int kTmemCols = 512;
 constexpr int kListMax = 4096;
@@ -83,10 +83,10 @@ struct Layout {
   static constexpr int kBytes = kBar + 512;
   static constexpr int kAlloc = kBytes + 1024;           // slack for 1024-byte alignment
   // mbarrier indices
-  static constexpr int q_full = 0;                       // + tile
+  static constexpr int q_full = 0;
   // + 2 * tile + half: each has one phase per key tile. (One barrier for both halves would let a warp that
   // is through with its second half arrive in the place of one that is still at its first.)
-  static constexpr int s_full = q_full + kTiles;
+  static constexpr int s_full = q_full + 1;
   static constexpr int p_full = s_full + 2 * kTiles;
   static constexpr int o_part = p_full + 2 * kTiles;     // + tile: the last step's first half is in O_t
   static constexpr int o_full = o_part + kTiles;         // + tile: all of O_t
@@ -98,8 +98,8 @@ struct Layout {
   static constexpr int c_empty = c_full + kCStages;
   static constexpr int drain = c_empty + kCStages;
   static_assert((drain + 1) * 8 <= 512, "barrier block");
-  static_assert(kAlloc <= 232448, "shared memory");
-  // the merge of the two tiles stages 128 fp32 rows over the V and K rings
+  static_assert(kAlloc + 1536 <= 232448, "shared memory, with the static part");
+  // the merge of the two tiles stages half of 2 x 128 fp32 rows over the V and K rings
   static_assert(!kOneSet || kVStages * kVTile + kKStages * kKTile >= kBM * D * 4, "merge staging");
 };
 
@@ -140,10 +140,11 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   constexpr int kIssuers = kOneSet ? kTiles : 1;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_row0, s_nrows;
+  __shared__ int s_run[2];
+  __shared__ float s_rowc[(kOneSet ? 1 : kTiles) * kBM];   // scale * log2(e) * 2^e of each row of Q
   __shared__ volatile int s_abort;
   __shared__ unsigned int s_wcnt[kThreads / 32];
-  __shared__ float2 s_ml[kOneSet ? kBM : 1];
+  constexpr int kChunks = D / 8;                    // 16-byte chunks of half a row of O
 
   const AttnArgs& p = prm.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -157,21 +158,21 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   if constexpr (kOneSet) {
     if (masked) {
       // lower bounds in idx of this query block and of the next (or of N)
-      if (warp == 0) {
-        const int64_t key = static_cast<int64_t>(blockIdx.x) * kBN;
-        const int64_t lo = warp_lower_bound(p.idx, rows, key, lane);
-        const int64_t n = warp_lower_bound(p.idx, rows, key + kBN < p.N ? key + kBN : p.N, lane) - lo;
-        if (lane == 0) {
-          s_row0 = static_cast<int>(lo);
-          s_nrows = static_cast<int>(n < 0 ? 0 : (n > kBM ? kBM : n));
-          // more rows than tokens (an index repeated), or entries outside [0, N): those rows are skipped
-          if (h == 0 && (n > kBM || (rows > 0 && blockIdx.x == 0 && (p.idx[0] < 0 || p.idx[rows - 1] >= p.N))))
-            raise_status(prm.status, STATUS_BOUNDS);
-        }
+      if (warp < 2) {
+        const int64_t key = (static_cast<int64_t>(blockIdx.x) + warp) * kBN;
+        const int64_t at = warp_lower_bound(p.idx, rows, key < p.N ? key : p.N, lane);
+        if (lane == 0) s_run[warp] = static_cast<int>(at);
+      } else if (warp == 2 && h == 0 && blockIdx.x == 0 && rows > 0 && lane == 0 &&
+                 (p.idx[0] < 0 || p.idx[rows - 1] >= p.N)) {
+        raise_status(prm.status, STATUS_BOUNDS);   // entries outside [0, N): those rows are skipped
       }
       __syncthreads();
-      row0 = s_row0;
-      nrows = s_nrows;
+      row0 = s_run[0];
+      nrows = s_run[1] - s_run[0];
+      if (nrows > kBM) {                           // more rows than tokens: an index repeated
+        if (tid == 0 && h == 0) raise_status(prm.status, STATUS_BOUNDS);
+        nrows = kBM;
+      }
     } else if (nrows > kBM) {
       nrows = kBM;
     }
@@ -195,8 +196,8 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   auto has_rows = [&](int t, int w) { return first_row(t, w) < (t ? rows_t1 : rows_t0) || first_row(t, w) == 0; };
   if (tid == 0) {
     s_abort = 0;
+    mbar_init(bar(L::q_full), kSoftmaxThreads);
     for (int t = 0; t < kTiles; ++t) {
-      mbar_init(bar(L::q_full + t), kOneSet ? kSoftmaxThreads : kBM);
       mbar_init(bar(L::o_part + t), 1);
       mbar_init(bar(L::o_full + t), 1);
       int warps = 0;                // that store P'_t
@@ -408,7 +409,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       bool ok = true;
       for (int t = t_lo; t < t_hi; ++t) {
         if (!ok || steps(t) == 0) continue;
-        ok = mbar_wait(bar(L::q_full + (kOneSet ? 0 : t)), 0, &s_abort, prm.status) && wait_k(seq(t, 0));
+        ok = mbar_wait(bar(L::q_full), 0, &s_abort, prm.status) && wait_k(seq(t, 0));
         tc_fence_after();
         if (!ok) continue;
         issue_s(t, 0, seq(t, 0) % L::kKStages);
@@ -449,60 +450,65 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     const bool valid = lrow < nrows;
     const int64_t row = row0 + lrow;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const bool works = has_rows(t, warp & 3);
 
-    // ---- this row of Q as hi + lo e4m3 codes (kOneSet: tile 0's warps store hi, tile 1's lo) ----------
-    float rowc = prm.scale_log2;
+    // ---- Q as hi + lo e4m3 codes: kLanesQ lanes per row, all softmax warps over all rows -------------------
     {
-      constexpr int kVec = D / 8;
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + (row * p.H + h) * D);
-      uint4 x[kVec];
-      float top = 0.f;
+      constexpr int kLanesQ = D / 8;                            // 8 channels each
+      constexpr int kRowsP = kSoftmaxThreads / kLanesQ;         // rows of a pass
+      constexpr int kAhead = 4;                                 // passes whose loads are in flight
+      const int lq = tid % kLanesQ;
+      const int need = (nrows + 31) & ~31;                      // the working warps' other lanes get zeros
+      for (int r0 = tid / kLanesQ; r0 < need; r0 += kAhead * kRowsP) {
+        uint4 x[kAhead];
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) x[i] = valid ? src[i] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float a = fabsf(bf16lo(w[k])), b = fabsf(bf16hi(w[k]));
-          if (a < INFINITY) top = fmaxf(top, a);
-          if (b < INFINITY) top = fmaxf(top, b);
+        for (int i = 0; i < kAhead; ++i) {
+          const int r = r0 + i * kRowsP;
+          x[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < nrows) x[i] = *(reinterpret_cast<const uint4*>(p.q + ((row0 + r) * p.H + h) * D) + lq);
         }
-      }
-      float sc = scale_of_amax(top);
-      if (sc == 0.f) sc = 1.f;
-      rowc *= sc;
-      const float inv = 1.f / sc;
-      uint8_t* part = gbase + L::kQ + (kOneSet ? 0 : t) * 2 * L::kQPart;
 #pragma unroll
-      for (int i = 0; i < kVec; i += 2) {          // 16 channels = one 16-byte chunk of codes
-        uint32_t hi[4], lo[4];
+        for (int i = 0; i < kAhead; ++i) {
+          const int r = r0 + i * kRowsP;
+          float f[8] = {bf16lo(x[i].x), bf16hi(x[i].x), bf16lo(x[i].y), bf16hi(x[i].y),
+                        bf16lo(x[i].z), bf16hi(x[i].z), bf16lo(x[i].w), bf16hi(x[i].w)};
+          float top = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint4 v = x[i + (k >> 1)];
-          const uint32_t w[2] = {(k & 1) ? v.z : v.x, (k & 1) ? v.w : v.y};
-          float f[4] = {bf16lo(w[0]) * inv, bf16hi(w[0]) * inv, bf16lo(w[1]) * inv, bf16hi(w[1]) * inv};
+          for (int c = 0; c < 8; ++c)
+            if (fabsf(f[c]) < INFINITY) top = fmaxf(top, fabsf(f[c]));
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (!(fabsf(f[c]) < INFINITY)) f[c] = NAN;     // an infinite logit makes the row NaN
-          hi[k] = pack_e4m3x4(f[0], f[1], f[2], f[3]);
-          const float2 a = f16x2_to_f2(e4m3x2_to_f16x2(hi[k])), b = f16x2_to_f2(e4m3x2_to_f16x2(hi[k] >> 16));
-          lo[k] = pack_e4m3x4(f[0] - a.x, f[1] - a.y, f[2] - b.x, f[3] - b.y);
+          for (int o = kLanesQ / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          float sc = scale_of_amax(top);
+          if (sc == 0.f) sc = 1.f;
+          const float inv = 1.f / sc;
+          uint32_t hi[2], lo[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float* g = f + 4 * k;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) g[c] = fabsf(g[c]) < INFINITY ? g[c] * inv : NAN;   // an infinite logit: NaN
+            hi[k] = pack_e4m3x4(g[0], g[1], g[2], g[3]);
+            const float2 a = f16x2_to_f2(e4m3x2_to_f16x2(hi[k])), b = f16x2_to_f2(e4m3x2_to_f16x2(hi[k] >> 16));
+            lo[k] = pack_e4m3x4(g[0] - a.x, g[1] - a.y, g[2] - b.x, g[3] - b.y);
+          }
+          if (r < need) {
+            const int rt = r & (kBM - 1), c = lq >> 1;          // row of its tile, 16-byte chunk
+            uint8_t* to = gbase + L::kQ + (r / kBM) * 2 * L::kQPart + 8 * (lq & 1) +
+                          (D == 128 ? rt * 128 + ((c ^ (rt & 7)) << 4) : rt * 64 + ((c ^ ((rt >> 1) & 3)) << 4));
+            *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(to + L::kQPart) = make_uint2(lo[0], lo[1]);
+            if (lq == 0) s_rowc[r] = prm.scale_log2 * sc;
+          }
         }
-        const int c = i >> 1;
-        const int off = D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-        if (!kOneSet || t == 0) *reinterpret_cast<uint4*>(part + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if (!kOneSet || t == 1)
-          *reinterpret_cast<uint4*>(part + L::kQPart + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
       fence_proxy_async_smem();
-      mbar_arrive(bar(L::q_full + (kOneSet ? 0 : t)));
+      mbar_arrive(bar(L::q_full));
+      barrier_softmax();                                        // s_rowc
     }
-
+    const float rowc = works ? s_rowc[lrow] : 1.f;
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     const int nsteps = steps(t);
-    const bool works = has_rows(t, warp & 3);
     auto scales = [&](int j, float& ks, float& vs) {
       const int64_t at = static_cast<int64_t>(key_tile(seq(t, j))) * p.H + h;
       ks = __ldg(prm.ks + at);
@@ -610,38 +616,37 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
     float w0 = 1.f, w1 = 0.f;                     // weights of this tile's and the other tile's sums
+    constexpr int kMine = kOneSet ? D / 2 : D;    // columns of the output that this thread writes, from c0
+    const int c0 = kOneSet ? t * kMine : 0;
     const float* other = nullptr;
     if constexpr (kOneSet) {
-      // tile 1 stages its row over the rings (free once both tiles' last products are complete),
-      // chunks rotated by row so the 16-byte accesses of a warp hit distinct banks
-      constexpr int kChunks = D / 4;
+      // Each tile stages the half of its row that the other will write over the rings (free once both tiles' last
+      // products are complete), chunks rotated by row so the 16-byte accesses of a warp hit distinct banks.
+      // With shifted lanes the two threads of a row sit in different warps: both have r.
       float4* stage = reinterpret_cast<float4*>(gbase + L::kV);
+      float2* s_ml = reinterpret_cast<float2*>(gbase + L::kList);   // [tile][row]; the list is done with
       barrier_softmax();
-      if (t == 1 && ok) {
-        s_ml[r] = make_float2(m_run, l_run);
-        if (works && nsteps > 0) {
+      s_ml[t * kBM + r] = make_float2(m_run, l_run);
+      if (ok && works && nsteps > 0) {
 #pragma unroll
-          for (int i0 = 0; i0 < D; i0 += 32) {
-            float o[32];
-            tmem_ld32(tO(t) + lane_off + i0, o);
+        for (int i0 = 0; i0 < kMine; i0 += 32) {
+          float o[32];
+          tmem_ld32(tO(t) + lane_off + (1 - t) * kMine + i0, o);
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              stage[r * kChunks + (i0 / 4 + q + r) % kChunks] =
-                  make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-          }
+          for (int q = 0; q < 8; ++q)
+            stage[(t * kBM + r) * kChunks + (i0 / 4 + q + r) % kChunks] =
+                make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
         }
       }
       barrier_softmax();
-      if (t == 1) return;
-      ok = ok && !s_abort;
-      ok = __all_sync(0xffffffffu, ok);
-      const float2 ml = s_ml[r];
+      ok = __all_sync(0xffffffffu, ok && !s_abort);
+      const float2 ml = s_ml[(1 - t) * kBM + r];
       const float m = fmaxf(m_run, ml.x);
       w0 = part_weight(m_run, l_run, m);
       w1 = part_weight(ml.x, ml.y, m);
-      l_run = w0 * l_run + (w1 != 0.f ? w1 * ml.y : 0.f);
+      l_run = (w0 != 0.f ? w0 * l_run : 0.f) + (w1 != 0.f ? w1 * ml.y : 0.f);
       m_run = m;
-      other = reinterpret_cast<const float*>(stage);
+      other = reinterpret_cast<const float*>(stage + (1 - t) * kBM * kChunks);
     }
     if (!ok || !works) return;
     // a row with no key has l = 0: o = 0, lse = -inf; a NaN sum stays NaN
@@ -652,15 +657,14 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     const int64_t orow = row * p.H + h;
     const int64_t prow = prm.nsplit > 1 ? static_cast<int64_t>(blockIdx.z) * prm.part_rows * p.H + orow - prm.part_row0 * p.H : 0;
 #pragma unroll
-    for (int i0 = 0; i0 < D; i0 += 32) {
+    for (int i0 = 0; i0 < kMine; i0 += 32) {
       float o[32];
       __syncwarp();
-      if (nsteps > 0) tmem_ld32(tO(t) + lane_off + i0, o);
+      if (nsteps > 0) tmem_ld32(tO(t) + lane_off + c0 + i0, o);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] = nsteps > 0 && l_run != 0.f ? o[i] * w0 : 0.f;
+      for (int i = 0; i < 32; ++i) o[i] = nsteps > 0 && w0 != 0.f ? o[i] * w0 : 0.f;
       if constexpr (kOneSet) {
         if (w1 != 0.f) {
-          constexpr int kChunks = D / 4;
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             const float4 x = reinterpret_cast<const float4*>(other)[r * kChunks + (i0 / 4 + q + r) % kChunks];
@@ -672,19 +676,21 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         }
       }
       if (valid && prm.nsplit > 1) {
-        float4* dst = reinterpret_cast<float4*>(prm.o_part + prow * D + i0);
+        float4* dst = reinterpret_cast<float4*>(prm.o_part + prow * D + c0 + i0);
 #pragma unroll
         for (int q = 0; q < 8; ++q) dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
       } else if (valid) {
-        uint4* dst = reinterpret_cast<uint4*>(p.o + orow * D + i0);
+        uint4* dst = reinterpret_cast<uint4*>(p.o + orow * D + c0 + i0);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           dst[q] = make_uint4(pack_bf16x2(o[8 * q], o[8 * q + 1]), pack_bf16x2(o[8 * q + 2], o[8 * q + 3]),
                               pack_bf16x2(o[8 * q + 4], o[8 * q + 5]), pack_bf16x2(o[8 * q + 6], o[8 * q + 7]));
       }
     }
-    if (valid && prm.nsplit > 1) prm.lse_part[prow] = lse;
-    else if (valid && p.lse) p.lse[orow] = lse;
+    if (valid && (!kOneSet || t == 0)) {
+      if (prm.nsplit > 1) prm.lse_part[prow] = lse;
+      else if (p.lse) p.lse[orow] = lse;
+    }
   };
 
   // teardown; each role runs its own copy (ptxas allots a region the registers of its setmaxnreg only
