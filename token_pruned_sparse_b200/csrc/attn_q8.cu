@@ -30,10 +30,22 @@
 //   two partial results are merged through shared memory at the end. A masked row set
 //   streams only the key tiles its query block keeps, so a block that is not kept is
 //   never read, whatever it holds.
-// Warps: 0-3 / 4-7 softmax of tile 0 / 1 (thread r = row r = TMEM lane r), 8-11 converters of V,
-// 12 TMA producer, 13 MMA issuer and TMEM owner, 14 MMA issuer of tile 1 (one set), the rest idle. Every mbarrier wait is bounded:
-// on expiry the CTA sets the device status word (TPS_ERR_TIMEOUT), drains what it
-// issued, frees TMEM and returns.
+// Warps: 0-3 / 4-7 softmax of tile 0 / 1 (one TMEM lane = one row per thread), 8-11 converters of V, 12 TMA
+// producer, 13 MMA issuer and TMEM owner, 14 MMA issuer of tile 1 (one set), 15 idle. Every wait is bounded: on
+// expiry the CTA sets the device status word (TPS_ERR_TIMEOUT), drains what it issued, frees TMEM and returns.
+//
+// What bounds it, and what the steps towards it measured (middle video, 6,084 rows x 20,280 keys, 12 heads, d =
+// 128, 0.758 TFLOP; single calls; clocks of an SM per step of 256 rows x 128 keys):
+//   MMAs alone: 2,484 clocks (S in halves of N = 64: 50.7 clocks each, bound by the shared-memory reads of Q;
+//   P' V 65.6 each); exp2 on 16 lanes a clock: 2,048.
+//   - first form, descriptors built before each MMA by "lane 0": 897 us (a step 4,900 clocks, the issuer 100
+//     clocks per MMA);
+//   - one elected thread and precomputed descriptors (22 clocks per MMA): 760 us;
+//   - S through the registers 32 columns at a time instead of 128 (no spills): 680 us;
+//   - S in two halves per tile, so that MMAs run under the exponentials: 620 us;
+//   - registers moved to the roles that spilled, Q's parts made by rows: 616 us = 1,230 TFLOP/s.
+// Back to back the GPU's power limit holds it to 700-715 us (1.70 GHz): the bf16 kernel takes 675 us there
+// and reads twice the cache.
 #include "attn_q8.cuh"
 #include "q8.cuh"
 #include "tc_ptx.cuh"
@@ -60,7 +72,7 @@ constexpr int kLaunchRegs = 128, kSoftmaxRegs = 144, kConvRegs = 104, kProducerR
 static_assert(8 * kSoftmaxRegs + 4 * kConvRegs + 4 * kProducerRegs <= 16 * kLaunchRegs, "register split");
 constexpr int kTmemCols = 512;
 constexpr int kListMax = 4096;
-constexpr float kSumLimit = 32768.f;   // largest tile row sum kept without a new maximum: P' stays finite in f16
+constexpr float kSumLimit = 32768.f;   // largest sum of a row's half tile kept without a new maximum: P' stays finite in f16
 static_assert(kBN == kScaleBlock, "a key tile has one scale");
 
 template <int D, bool kOneSet>
