@@ -160,18 +160,24 @@ __global__ void __launch_bounds__(kThreads, kSets == 1 ? 3 : 2) attn_q8_few_kern
 
   auto step = [&](const Codes& c, int64_t key0, const float (&cc)[2], float lv, float ivs) {
     // ---- S = Q K^T: sf[n] = rows g, g + 8 x keys 8 n + 2t, 8 n + 2t + 1 -----------------------------
-    float sf[2][4];
+    // (even and odd steps apart: the four chains of products are half as long)
+    float sf[2][4], sg[2][4];
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) sf[n][k] = 0.f;
+      for (int k = 0; k < 4; ++k) sf[n][k] = sg[n][k] = 0.f;
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
         const uint4 x = c.k[n][s >> 2];
         const uint32_t w = (s & 3) == 0 ? x.x : ((s & 3) == 1 ? x.y : ((s & 3) == 2 ? x.z : x.w));
-        mma_f16(sf[n], qf[s], e4m3x2_to_f16x2(w), e4m3x2_to_f16x2(w >> 16));
+        mma_f16((s & 1) ? sg[n] : sf[n], qf[s], e4m3x2_to_f16x2(w), e4m3x2_to_f16x2(w >> 16));
       }
-    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sf[n][k] += sg[n][k];
     const bool whole = key0 + kKeys <= p.N;
     if (!whole) {
 #pragma unroll
