@@ -470,7 +470,8 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       constexpr int kRowsP = kSoftmaxThreads / kLanesQ;         // rows of a pass
       constexpr int kAhead = 4;                                 // passes whose loads are in flight
       const int lq = tid % kLanesQ;
-      const int need = (nrows + 31) & ~31;                      // the working warps' other lanes get zeros
+      // the working warps' other lanes get zeros (warp 0 of a tile without rows included)
+      const int need = kOneSet || nrows > kBM ? (nrows + 31) & ~31 : kBM + 32;
       for (int r0 = tid / kLanesQ; r0 < need; r0 += kAhead * kRowsP) {
         uint4 x[kAhead];
 #pragma unroll
