@@ -414,7 +414,10 @@ TPS_API int pruned_attn_mma(const tps_bf16* q_act, const tps_bf16* k, const tps_
 /* pruned_attn over a cache held in 8 bits (the layout of kv_sync_q8):
  *   o_act[j,h] = sum_n softmax_n(scale * q_act[j,h] . k[n,h]) v[n,h],
  *   k[n,h] = k_cache[n,h] * k_scale[n / 128][h], v likewise,
- * with the blockmask, lse and empty-row rules of pruned_attn. Scales must be finite
+ * with the blockmask, lse and empty-row rules of pruned_attn. With a mask, idx must be
+ * ascending and unique; rows whose entry lies outside [0, N), and a block's rows beyond
+ * 128, are left as they were and flagged (TPS_ERR_BOUNDS at tps_check). Without a mask idx
+ * is not read. Rows j >= min(*count, cap) of o_act and lse are left as they were. Scales must be finite
  * and >= 0 (a scale of 0 stands for values of 0), the non-zero v_scale within
  * [2^-100, 2^100]. The codes are used as they are: Q enters the e4m3 products as two
  * e4m3 parts (exact for channels down to 2^-10 of a row's largest), the

@@ -543,6 +543,127 @@ def test_another_stream_a_captured_step_and_repeats_agree():
             assert torch.equal(a, b)
 
 
+def test_two_streams_at_once():
+    """Calls in flight on two streams share nothing: each gives what it gives alone."""
+    jobs = []
+    for N, A, H, d, seed in ((3000, 700, 3, 128, 1), (6000, 9, 5, 64, 2)):
+        cache, q, idx = _attn_case(N, A, H, d, seed)
+        jobs.append((q.to(DEV), _to_dev(cache), _dev(idx), 1.0 / math.sqrt(d), torch.cuda.Stream()))
+    alone = [tps.pruned_attn_q8(q, *c, *i, s) for q, c, i, s, _ in jobs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for k, (q, c, i, s, st) in enumerate(jobs):
+            with torch.cuda.stream(st):
+                got[k].append(tps.pruned_attn_q8(q, *c, *i, s))
+    torch.cuda.synchronize()
+    tps.tps_check()
+    for a, outs in zip(alone, got):
+        assert all(torch.equal(a, o) for o in outs)
+    # the same with the stream given by argument, and as a raw handle
+    q, c, i, s, st = jobs[0]
+    for handle in (st, st.cuda_stream):
+        o = torch.empty_like(q)
+        st.wait_stream(torch.cuda.current_stream())
+        tps.pruned_attn_q8(q, *c, *i, s, o_act=o, stream=handle)
+        torch.cuda.current_stream().wait_stream(st)
+        assert torch.equal(o, alone[0])
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_outputs_made_for_another_stream_wait_for_the_memory(raw):
+    """With stream= given, an output may get memory that the current stream still reads: the call waits for it."""
+    grid, H, d = (5, 20, 20), 4, 128
+    N, dims = 2000, synth.rope_dims(128)
+    table = tps.rope_table(dims, grid)
+    cache, q, idx = _attn_case(N, N, H, d, 11)
+    q, cache, idx = q.to(DEV), _to_dev(cache), _dev(idx)
+    other = torch.cuda.Stream()
+    want = tps.rope_rows(q, None, None, table, dims, grid)
+    want_o = tps.pruned_attn_q8(q, *cache, *idx, 0.1)
+    torch.cuda.synchronize()
+    for call, ref in ((lambda st: tps.rope_rows(q, None, None, table, dims, grid, stream=st), want),
+                      (lambda st: tps.pruned_attn_q8(q, *cache, *idx, 0.1, stream=st), want_o)):
+        victim = torch.full_like(q, 3.0)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)            # about 10 ms ahead of the read of victim
+        read = victim + 1.0
+        del victim
+        out = call(other.cuda_stream if raw else other)
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)
+        assert bool((read == 4.0).all())
+    tps.tps_check()
+
+
+def test_two_captured_graphs_share_a_workspace_and_one_makes_its_own():
+    N, A, H, d = 4000, 100, 3, 128               # few rows of work: the keys are split
+    ws = tps.attn_q8_workspace(A, N, H, d)
+    assert ws.numel() > 0
+    jobs = []
+    for seed in (1, 2, 3):
+        cache, q, idx = _attn_case(N, A, H, d, seed)
+        q, cache, idx = q.to(DEV), _to_dev(cache), _dev(idx)
+        want = tps.pruned_attn_q8(q, *cache, *idx, 0.1)
+        o, g = torch.empty_like(q), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            tps.pruned_attn_q8(q, *cache, *idx, 0.1, o_act=o, ws=None if seed == 3 else ws)
+        jobs.append((g, o, want, (q, cache, idx)))
+    for _ in range(3):
+        for g, o, *_ in jobs:
+            o.fill_(float("nan"))
+        for g, *_ in jobs:                       # one after the other on one stream
+            g.replay()
+        torch.cuda.synchronize()
+        for _, o, want, _ in jobs:
+            assert torch.equal(o, want)
+    tps.tps_check()
+
+
+def test_empty_lists_and_zero_capacity():
+    H, d, N = 2, 64, 200
+    cache, q, _ = _attn_case(N, 5, H, d, 4)
+    cache, q = _to_dev(cache), q.to(DEV)
+    before = [t.view(torch.uint8).clone() for t in cache]
+    none = (torch.empty(0, dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV))
+    empty = q[:0]
+    assert tps.pruned_attn_q8(empty, *cache, *none, 0.1).shape == (0, H, d)
+    tps.kv_sync_q8(*cache, empty, empty, *none)
+    dims, grid = synth.rope_dims(64), (1, 10, 20)
+    assert tps.rope_rows(empty, *none, tps.rope_table(dims, grid), dims, grid).shape == (0, H, d)
+    o = torch.full_like(q, 7.0)
+    tps.pruned_attn_q8(q, *cache, *_dev(np.arange(5), 0), 0.1, o_act=o)      # capacity 5, none active
+    tps.kv_sync_q8(*cache, q, q, *_dev(np.arange(5), 0))
+    assert bool((o == 7.0).all())
+    assert all(torch.equal(a, b.view(torch.uint8)) for a, b in zip(before, cache))
+    tps.tps_check()
+
+
+def test_a_chunk_of_frames_with_an_origin():
+    """Streaming: a window of the video, its first frame at position 7, gives the keys of the whole video's table."""
+    H, d, grid = 2, 128, (3, 4, 5)
+    N, dims = 60, synth.rope_dims(128)
+    k = synth.gaussian_bf16((N, H, d), 5)
+    every = torch.arange(N, dtype=torch.int32, device=DEV)
+    count = torch.tensor([N], dtype=torch.int32, device=DEV)
+    got = []
+    long_grid = (10, 4, 5)
+    for table, g, shift in ((tps.rope_table(dims, grid, origin=(7, 0, 0)), grid, 0),
+                            (tps.rope_table(dims, long_grid), long_grid, 7 * 20)):
+        n = g[0] * g[1] * g[2]
+        cache = tps.cache_q8(n, H, d)
+        tps.kv_sync_q8(*cache, k.to(DEV), k.to(DEV), every + shift, count, rope=(table, dims, g))
+        got.append((tps.rope_rows(k.to(DEV), every + shift, count, table, dims, g), cache))
+    tps.tps_check()
+    assert torch.equal(got[0][0], got[1][0])
+    a = Q.q8_values(got[0][1][0].cpu().view(torch.uint8).numpy(), got[0][1][2].cpu().numpy())
+    b = Q.q8_values(got[1][1][0].cpu().view(torch.uint8).numpy(), got[1][1][2].cpu().numpy())[140:200]
+    # the same values on grids whose scales may differ by a power of two: equal where both are normal
+    big = np.abs(a) >= 2.0 ** -6 * np.maximum(got[0][1][2].cpu().numpy().max(), got[1][1][2].cpu().numpy().max())
+    np.testing.assert_array_equal(a[big], b[big])
+
+
 def test_offsets_beyond_32_bits():
     """A cache of more than 2^32 code bytes: the last blocks are written and attended at their own place."""
     H, d = 128, 128

@@ -380,6 +380,20 @@ def _call(fn, index, stream, *args):
         _chk(code)
 
 
+def _made_for(stream, index, *made):
+    """Tells torch's allocator that tensors made by this call are used on `stream`. It hands memory on in the
+    order of the current stream, so the other stream also waits for that one first."""
+    if stream is None:
+        return
+    on = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), index)
+    now = torch.cuda.current_stream(index)
+    if on.cuda_stream == now.cuda_stream:
+        return
+    on.wait_stream(now)
+    for t in made:
+        t.record_stream(on)
+
+
 class RopeGrid(C.Structure):
     """tps_rope_grid: channels and positions of the t, x, y axes, and the table."""
     _fields_ = [("dims", C.c_int32 * 3), ("size", C.c_int32 * 3), ("table", C.c_void_p)]
@@ -425,14 +439,17 @@ def rope_rows(src, idx, count, table, dims, grid, dst=None, src2=None, dst2=None
     A, H, d = shape
     dev = src.get_device()
     a_src = _check(who, "src", src, _BF16, shape, dev)
+    made = []
     if dst is None:
         dst = torch.empty_like(src)
+        made.append(dst)
     a_dst = _check(who, "dst", dst, _BF16, shape, dev)
     a_src2 = a_dst2 = None
     if src2 is not None:
         a_src2 = _check(who, "src2", src2, _BF16, shape, dev)
         if dst2 is None:
             dst2 = torch.empty_like(src2)
+            made.append(dst2)
         a_dst2 = _check(who, "dst2", dst2, _BF16, shape, dev)
     elif dst2 is not None:
         raise TPSError(INVALID_ARG, "rope_rows: dst2 without src2")
@@ -446,6 +463,8 @@ def rope_rows(src, idx, count, table, dims, grid, dst=None, src2=None, dst2=None
         return dst if src2 is None else (dst, dst2)
     g = _rope_grid(who, table, dims, grid, dev)
     F, Hs, Ws = grid
+    if made:
+        _made_for(stream, dev, *made)
     _call(lib().rope_rows, dev, stream, a_dst, a_src, a_dst2, a_src2, a_idx, a_cnt, cap, F * Hs * Ws, H, d,
           C.addressof(g), 1 if inverse else 0)
     return dst if src2 is None else (dst, dst2)
@@ -505,8 +524,10 @@ def pruned_attn_q8(q_act, k_cache, v_cache, k_scale, v_scale, idx, count, scale,
     N, H, d, dev, a_kc, a_vc, a_ks, a_vs = _cache_q8(who, k_cache, v_cache, k_scale, v_scale)
     rows = _rows_of(who, "q_act", q_act, H, d)
     a_q = _check(who, "q_act", q_act, _BF16, (rows, H, d), dev)
+    made = []
     if o_act is None:
         o_act = torch.empty_like(q_act)
+        made.append(o_act)
     n = _rows_of(who, "o_act", o_act, H, d)
     a_o = _check(who, "o_act", o_act, _BF16, (n, H, d), dev)
     rows = min(rows, n)
@@ -533,14 +554,11 @@ def pruned_attn_q8(q_act, k_cache, v_cache, k_scale, v_scale, idx, count, scale,
             with torch.cuda.device(dev):
                 n_ws = lib().tps_attn_q8_workspace_size(cap, N, H, d)
         if n_ws:
-            # the allocator hands the block on in the order of the current stream: for another stream
-            # it has to be told that the block is in use there
             ws = torch.empty(n_ws, dtype=torch.uint8, device=q_act.device)
             a_ws = ws.data_ptr()
-            if stream is not None:
-                on = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), dev)
-                on.wait_stream(torch.cuda.current_stream(dev))
-                ws.record_stream(on)
+            made.append(ws)
+    if made:
+        _made_for(stream, dev, *made)
     _call(lib().pruned_attn_q8, dev, stream, a_q, a_kc, a_vc, a_ks, a_vs, a_idx, a_cnt, cap, N, H, d, scale, a_mask,
           block, a_o, a_lse, a_ws, n_ws)
     return o_act
