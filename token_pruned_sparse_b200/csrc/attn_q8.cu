@@ -818,8 +818,9 @@ size_t ws_bytes_of(const Plan& plan, int64_t cap, int H, int d) {
   return (rows * d * sizeof(float) + 255) / 256 * 256 + rows * sizeof(float);
 }
 
-// The S-way merge of the partials: o = sum_s w_s o_s / sum_s w_s with w_s = exp(lse_s - max). A quarter-row of
-// 16-byte loads per thread; S loads in flight.
+// The S-way merge of the partials: o = sum_s w_s o_s / sum_s w_s with w_s = exp(lse_s - max). Latency is all it
+// costs, so a thread (4 channels of a row) loads values and statistics of 8 parts at a time, guarded rather than
+// in a remainder loop, against a running maximum.
 template <int D>
 __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Q8Args prm) {
   asm volatile("griddepcontrol.wait;" ::: "memory");   // launched ahead of the partials' end
@@ -827,31 +828,39 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Q8Ar
   const int64_t rows = active_count(p.count, p.cap) - prm.part_row0;
   const int64_t plane = prm.part_rows * p.H;
   const int64_t total = rows * p.H * (D / 4);
+  constexpr int kParts = 8;                            // loads in flight
   const float4* op = reinterpret_cast<const float4*>(prm.o_part);
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
        i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
     const int64_t rh = i / (D / 4);
-    float m = -INFINITY, nan = 0.f;
-#pragma unroll 8
-    for (int s = 0; s < prm.nsplit; ++s) {
-      const float l = prm.lse_part[s * plane + rh];
-      if (l != l) nan = l;
-      m = fmaxf(m, l);
-    }
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-    const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll 8
-    for (int s = 0; s < prm.nsplit; ++s) {
-      const float4 x = op[s * plane * (D / 4) + i];       // (zeros where a part has no key)
-      const float w = expf(prm.lse_part[s * plane + rh] - ref);
-      a.x = fmaf(w, x.x, a.x);
-      a.y = fmaf(w, x.y, a.y);
-      a.z = fmaf(w, x.z, a.z);
-      a.w = fmaf(w, x.w, a.w);
-      sum += w;
+    float m = -INFINITY, ref = 0.f, sum = 0.f;
+    for (int s0 = 0; s0 < prm.nsplit; s0 += kParts) {
+      float4 x[kParts];
+      float l[kParts];
+#pragma unroll
+      for (int u = 0; u < kParts; ++u) {
+        const bool in = s0 + u < prm.nsplit;
+        x[u] = in ? op[(s0 + u) * plane * (D / 4) + i] : make_float4(0.f, 0.f, 0.f, 0.f);
+        l[u] = in ? prm.lse_part[(s0 + u) * plane + rh] : -INFINITY;   // (a part without a key: zeros and -inf)
+      }
+      const float was = m;
+#pragma unroll
+      for (int u = 0; u < kParts; ++u) m = fmaxf(m, l[u]);              // NaN is passed over here, not by w
+      ref = m == -INFINITY ? 0.f : m;
+      const float f = expf(was - ref);
+      a = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
+      sum *= f;
+#pragma unroll
+      for (int u = 0; u < kParts; ++u) {
+        const float w = expf(l[u] - ref);
+        a.x = fmaf(w, x[u].x, a.x);
+        a.y = fmaf(w, x[u].y, a.y);
+        a.z = fmaf(w, x[u].z, a.z);
+        a.w = fmaf(w, x[u].w, a.w);
+        sum += w;
+      }
     }
-    sum += nan;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int64_t orow = prm.part_row0 * p.H + rh;
     reinterpret_cast<uint2*>(p.o + orow * D)[i % (D / 4)] =
