@@ -766,8 +766,11 @@ int smem_attribute(int bytes) {
 // How a call runs. A unit of work is one row tile (256 rows, or one set of 128) of one head; U units on P SMs
 // take ceil(U / P) unit times. Two ways out of a mostly empty last wave: all units split S ways along the
 // keys, or the units of the full waves whole and the remaining tiles split S_t ways in a second launch.
-// Costs in steps of key tiles: a CTA of n steps takes n + kEnds (prologue and epilogue); a split pays
-// the merge launch, and the merge's traffic grows with S, so a plan must gain 2% on the one before it.
+// Costs in steps of key tiles (of a pair of them in the one-set layout; 1.7 us each): a CTA of n steps takes
+// n + kEnds (prologue and epilogue), a split adds the merge. A plan must gain 2% on the one before it. Ranges of
+// down to two key tiles pay: 64 rows x 4,096 keys, 12 heads, took 16.3 us in 4 ranges of 8 tiles and take 13.5 in 8 of 4;
+// 67 x 11,501, 5 heads x 64: 18.1 us in 11, 13.9 in 23 (steps counted whole: 15.2 in 22). A second wave does not:
+// 128 x 32,760, 5 heads: 20.6 us in 29 ranges, 32.3 in 32.
 // Masked calls are one CTA per query block and head.
 struct Plan {
   bool few;             // the kernel of attn_q8_few.cu
@@ -775,33 +778,33 @@ struct Plan {
   int split;            // of the launch that has all tiles (main_tiles = 0), or of the tail
   int64_t main_tiles;   // tiles of an unsplit first launch; 0: none
 };
-constexpr double kEnds = 6.0, kMerge = 3.0;
-constexpr int kMaxSplit = 32;
+constexpr double kEnds = 6.0, kMerge = 1.5, kPart = 0.06;
+constexpr int kMaxSplit = 64;
 
 Plan make_plan(int64_t cap, int64_t N, int H, bool masked) {
   Plan best{!masked && cap <= kFewRows, masked || cap <= kBM, 1, 0};
   if (masked || cap < 1) return best;
   if (best.few) {
-    best.split = few_split(N, H);
+    best.split = few_split(cap, N, H);
     return best;
   }
   const int64_t tiles = best.one_set ? 1 : (cap + kTiles * kBM - 1) / (kTiles * kBM);
   const int64_t units = tiles * H;
   const int64_t nkt = (N + kBN - 1) / kBN;
-  const double steps = best.one_set ? nkt / 2.0 : static_cast<double>(nkt);
   const int64_t P = sm_count();
   auto cost_of = [&](int64_t u, int s) {
-    return static_cast<double>((u * s + P - 1) / P) * (steps / s + kEnds) + (s > 1 ? kMerge : 0.0);
+    const int64_t own = (nkt + s - 1) / s, steps = best.one_set ? (own + 1) / 2 : own;
+    return static_cast<double>((u * s + P - 1) / P) * (steps + kEnds) + (s > 1 ? kMerge + kPart * s : 0.0);
   };
   double cost = 1e300;
-  for (int s = 1; s <= kMaxSplit && (s == 1 || nkt >= 8 * s); ++s)
+  for (int s = 1; s <= kMaxSplit && (s == 1 || nkt >= 2 * s); ++s)
     if (const double c = cost_of(units, s); c < 0.98 * cost) {
       cost = c;
       best.split = s;
     }
   const int64_t whole = units / P * P / H;          // tiles that fit the full waves
   if (whole >= 1 && whole < tiles)
-    for (int s = 2; s <= kMaxSplit && nkt >= 8 * s; ++s)
+    for (int s = 2; s <= kMaxSplit && nkt >= 2 * s; ++s)
       if (const double c = cost_of(whole * H, 1) + cost_of((tiles - whole) * H, s); c < 0.98 * cost) {
         cost = c;
         best.split = s;

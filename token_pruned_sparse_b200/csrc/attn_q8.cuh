@@ -34,7 +34,7 @@ __device__ __forceinline__ float part_weight(float m_part, float l_part, float m
 // At most kFewRows rows of a dense call (attn_q8_few.cu).
 constexpr int kFewRows = 16;
 constexpr int kFewMaxSplit = 128;
-int few_split(int64_t N, int H);
+int few_split(int64_t cap, int64_t N, int H);
 int launch_attn_q8_few(const Q8Args& prm, cudaStream_t st);
 
 }  // namespace tps

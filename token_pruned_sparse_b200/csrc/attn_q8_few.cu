@@ -45,9 +45,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+// 8-row sets of a call, and the CTAs that an SM holds (by registers)
+constexpr int few_sets(int64_t cap) { return cap <= 8 ? 1 : 2; }
+constexpr int few_ctas(int sets) { return sets == 1 ? 3 : 2; }
+
 // kSets: 8-row sets (1 or 2).
 template <int D, int kSets>
-__global__ void __launch_bounds__(kThreads, kSets == 1 ? 3 : 2) attn_q8_few_kernel(const __grid_constant__ Q8Args prm) {
+__global__ void __launch_bounds__(kThreads, few_ctas(kSets)) attn_q8_few_kernel(const __grid_constant__ Q8Args prm) {
   constexpr int kSteps = D / 16;        // 16-channel steps of S
   constexpr int kTilesM = D / 16;       // 16-channel tiles of O^T
   constexpr int kKV = D / 64;           // 16-byte vectors of a thread's key (4 threads hold D channels)
@@ -333,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, kSets == 1 ? 3 : 2) attn_q8_few_kern
 
 int launch_attn_q8_few(const Q8Args& prm, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>(prm.a.H), static_cast<unsigned>(prm.nsplit));
-  const bool one = prm.a.cap <= 8;
+  const bool one = few_sets(prm.a.cap) == 1;
   if (prm.a.d == 128 && one) attn_q8_few_kernel<128, 1><<<grid, kThreads, 0, st>>>(prm);
   else if (prm.a.d == 128) attn_q8_few_kernel<128, 2><<<grid, kThreads, 0, st>>>(prm);
   else if (one) attn_q8_few_kernel<64, 1><<<grid, kThreads, 0, st>>>(prm);
@@ -341,13 +345,27 @@ int launch_attn_q8_few(const Q8Args& prm, cudaStream_t st) {
   return launch_status("pruned_attn_q8");
 }
 
-// Key ranges of a head: about three CTAs per SM, each warp with 2 blocks or more.
-int few_split(int64_t N, int H) {
+// Key ranges of a head, from the time in units of a warp's block (2.6 us while latency counts): waves of CTAs times
+// the most blocks of a warp and kEnds for the rest of a CTA, and the merge. One block a warp is enough: 8 rows x 64
+// over 11,501 keys, 5 heads, took 12.7 us in 11 ranges (3 blocks) and take 8.7 us in 23 (one). A wave that is
+// not full costs more than longer ranges: 16 rows (2 CTAs per SM) over 118,800 keys, 24 heads: 157 us in 12 ranges,
+// 187 us in 18.
+int few_split(int64_t cap, int64_t N, int H) {
+  constexpr double kEnds = 2.0, kMerge = 0.6, kPart = 0.03;
   const int64_t nb = (N + kScaleBlock - 1) / kScaleBlock;
-  int64_t s = (static_cast<int64_t>(sm_count()) * 3) / H;
-  const int64_t most = nb / (2 * kWarps);
-  s = s < most ? s : most;
-  return static_cast<int>(s < 1 ? 1 : (s > kFewMaxSplit ? kFewMaxSplit : s));
+  const int64_t resident = static_cast<int64_t>(sm_count()) * few_ctas(few_sets(cap));
+  int best = 1;
+  double cost = 1e300;
+  for (int s = 1; s <= kFewMaxSplit && (s == 1 || s * kWarps < nb + kWarps); ++s) {
+    const int64_t waves = (static_cast<int64_t>(H) * s + resident - 1) / resident;
+    const int64_t blocks = ((nb + s - 1) / s + kWarps - 1) / kWarps;
+    const double c = static_cast<double>(waves) * (blocks + kEnds) + (s > 1 ? kMerge + kPart * s : 0.0);
+    if (c < cost) {
+      cost = c;
+      best = s;
+    }
+  }
+  return best;
 }
 
 }  // namespace tps
