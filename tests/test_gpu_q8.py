@@ -698,3 +698,34 @@ def test_offsets_beyond_32_bits():
     ref, _ = O.pruned_attn(qh, kd[:, None].numpy(), vd[:, None].numpy(), idx[few], scale)
     ot, _ = Q.q8_attn_bound(qh, kd[:, None].numpy(), vd[:, None].numpy(), vs[:, h:h + 1].cpu().double().numpy(), idx[few], scale)
     assert np.all(np.abs(O.f64(o[:, h:h + 1].cpu()) - ref) <= ot)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("A,keep", [(900, 11), (900, 3), (100, 0), (17, 0)])
+def test_attn_q8_one_set_calls_repeat_bit_for_bit_beside_a_copy(A, keep, d):
+    """Calls whose two issuers share the key ring, over a cache that a copy on another stream drives out of L2: a load
+    may land late, and every call still gives the same bits, within the bound."""
+    N, H = 6000, 4
+    cache, q, idx = _attn_case(N, A, H, d, 29)
+    nb = (N + 127) // 128
+    bm = (np.random.default_rng(keep).random((nb, nb)).argsort(1) < keep).astype(np.uint8) if keep else None
+    scale = 1.0 / math.sqrt(d)
+    o, lse = _run_attn(cache, q, idx, scale, bm=bm)
+    _check_attn(o, lse, cache, q, idx, scale, bm)
+    qd, dev, act = q.to(DEV), _to_dev(cache), _dev(idx)
+    mask = None if bm is None else torch.from_numpy(bm).to(DEV)
+    ws = None if keep else tps.attn_q8_workspace(A, N, H, d)
+    big, other = torch.zeros(1 << 28, dtype=torch.uint8, device=DEV), torch.cuda.Stream()
+    to = torch.empty_like(big)
+    want, bad = torch.from_numpy(o).bfloat16().to(DEV), torch.zeros((), dtype=torch.int64, device=DEV)
+    got = torch.empty_like(qd)
+    torch.cuda.synchronize()
+    for i in range(1500):
+        if i % 3 == 0:
+            with torch.cuda.stream(other):
+                to.copy_(big)
+        tps.pruned_attn_q8(qd, *dev, *act, scale, blockmask=mask, o_act=got, ws=ws)
+        bad += (got != want).sum()
+    torch.cuda.synchronize()
+    tps.tps_check()
+    assert int(bad) == 0

@@ -77,11 +77,16 @@ static_assert(kBN == kScaleBlock, "a key tile has one scale");
 
 template <int D, bool kOneSet>
 struct Layout {
-  static constexpr int kKStages = D == 64 ? 4 : 3;
+  // A wait on a barrier's parity tells a phase from its neighbours only: a role must have seen phase n of a
+  // stage before it waits for phase n + 1. With one set the two issuers take alternate tiles and each waits
+  // for its own alone, so their rings (K, V) have an even number of stages: a stage then belongs to one issuer.
+  // (With three K stages issuer 1 could take tile 0's stage for tile 3's before tile 0 had landed.)
+  static constexpr int kKStages = D == 64 || kOneSet ? 4 : 3;
   static constexpr int kVStages = D == 64 ? 4 : (kOneSet ? 2 : 3);
+  static_assert(!kOneSet || (kKStages % kTiles == 0 && kVStages % kTiles == 0), "a stage belongs to one issuer");
   // kOneSet: V's codes come through a ring of their own, so that enough bytes are in flight to stream a
   // long cache for few rows (one tile ahead in the converters' registers reached 2.2 TB/s)
-  static constexpr int kCStages = kOneSet ? (D == 64 ? 6 : 4) : 0;
+  static constexpr int kCStages = kOneSet ? (D == 64 ? 6 : 3) : 0;
   static constexpr int kQPart = kBM * D;                 // one e4m3 tile
   static constexpr int kKTile = kBN * D;
   static constexpr int kSub = kBN * 128;                 // [128 keys x 64 f16], 128-byte swizzle
