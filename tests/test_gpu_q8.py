@@ -729,3 +729,32 @@ def test_attn_q8_one_set_calls_repeat_bit_for_bit_beside_a_copy(A, keep, d):
     torch.cuda.synchronize()
     tps.tps_check()
     assert int(bad) == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("A", [3, 16, 60, 300])
+@pytest.mark.parametrize("split", [False, True])
+def test_attn_q8_nan_values_reach_every_row_however_small_their_weight(d, A, split):
+    """A NaN code of V makes its channel NaN in every row that attends it, also where its key range, stream or warp has
+    a weight that is zero in fp32 (256 nats and more below the others)."""
+    N, H = 20 * 128 - 5, 1
+    rng = np.random.default_rng(5)
+    u = rng.choice([-1.0, 1.0], d)
+    low = (np.arange(N) // 128 % 2 == 1) | (np.arange(N) < 512)       # odd blocks, and the first four
+    k = np.where(low, -16.0, 16.0)[:, None, None] * u
+    v = rng.standard_normal((N, H, d))
+    zero = (np.zeros((N, H, d)), np.zeros((20, H)))
+    cache = [Q.kv_sync_q8(*zero, x, np.arange(N)) for x in (k, v)]
+    q = torch.from_numpy(np.broadcast_to(u, (A, H, d)).copy()).bfloat16()
+    idx = _idx(N, A, 3)
+    ws = None if split else torch.empty(0, dtype=torch.uint8, device=DEV)
+    scale = 0.125
+    o, lse = _run_attn(cache, q, idx, scale, ws=ws)
+    _check_attn(o, lse, cache, q, idx, scale)
+    for b in (0, 1, 5, 19):                                           # all of them low
+        dev = list(_to_dev(cache))
+        dev[1][b * 128 + 7, 0, 9] = 0x7F
+        got, glse = _run_attn(cache, q, idx, scale, dev=dev, ws=ws)
+        assert np.isnan(got[:, 0, 9]).all(), b
+        rest = np.delete(np.arange(d), 9)
+        assert np.array_equal(got[..., rest], o[..., rest]) and np.array_equal(glse, lse)

@@ -680,9 +680,9 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       __syncwarp();
       if (nsteps > 0) tmem_ld32(tO(t) + lane_off + c0 + i0, o);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] = nsteps > 0 && w0 != 0.f ? o[i] * w0 : 0.f;
+      for (int i = 0; i < 32; ++i) o[i] = nsteps > 0 ? o[i] * w0 : 0.f;   // (a weight of 0 keeps a NaN of V)
       if constexpr (kOneSet) {
-        if (w1 != 0.f) {
+        if (steps(1 - t) > 0) {
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             const float4 x = reinterpret_cast<const float4*>(other)[r * kChunks + (i0 / 4 + q + r) % kChunks];

@@ -310,8 +310,7 @@ __global__ void __launch_bounds__(kThreads, few_ctas(kSets)) attn_q8_few_kernel(
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float2 ml = s_ml[w][r];
-      const float f = part_weight(ml.x, ml.y, m);
-      if (f == 0.f) continue;
+      const float f = part_weight(ml.x, ml.y, m);        // (a weight of 0 keeps a NaN of V)
       const float4 x = *reinterpret_cast<const float4*>(&s_o[w][r][4 * c4]);
       a.x = fmaf(f, x.x, a.x);
       a.y = fmaf(f, x.y, a.y);
