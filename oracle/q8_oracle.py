@@ -90,7 +90,7 @@ def kv_sync_q8(values, scale, fresh, idx):
     return values, scale
 
 
-def q8_attn_bound(q, k, v, vs, idx, scale: float, blockmask=None):
+def q8_attn_bound(q, k, v, vs, idx, scale: float, blockmask=None, floor=None):
     """(tolerance of o [A, H, d], tolerance of lse [A, H]) for float64 k, v [N, H, d] and V's scales vs [nb, H].
 
     With E the mean over the softmax weights p, and e the relative error of an unrounded probability:
@@ -99,7 +99,9 @@ def q8_attn_bound(q, k, v, vs, idx, scale: float, blockmask=None):
               + 2^-22 (|x| + 4)                                       (the fp32 exponent, exp2, reciprocals),
       o:   (2^-11 + 2 e) E|v| + N 2^-25 448 max vs + 2^-8 |o|         (f16 probabilities, normal and below
               2^-14 of the reference; bf16 output),
-      lse: e + 2^-22 (|lse| + 1)."""
+      lse: e + 2^-22 (|lse| + 1).
+    floor: a tighter second term, for scales far apart and for long caches. What f16 cannot hold is below `floor` of
+    the row's largest p vs, so the term is N floor 448 max_n(p_n vs_n)."""
     A, H, d = q.shape
     N = k.shape[0]
     o_tol, l_tol = np.zeros((A, H, d)), np.zeros((A, H))
@@ -120,8 +122,11 @@ def q8_attn_bound(q, k, v, vs, idx, scale: float, blockmask=None):
         e = scale * (2.0 ** -17 * np.abs(Q).max(1) * np.abs(K).sum(1).max() + 2 * d * 2.0 ** -23 * ab.max(1))
         e = e + 2.0 ** -22 * (big + 4)
         o = p @ V
-        o_tol[:, h] = ((2.0 ** -11 + 2 * e)[:, None] * (p @ np.abs(V)) + N * 2.0 ** -25 * 448 * f64(vs)[:, h].max()
-                       + 2.0 ** -8 * np.abs(o))
+        if floor is None:
+            lost = N * 2.0 ** -25 * 448 * f64(vs)[:, h].max()
+        else:
+            lost = (N * floor * 448 * (p * f64(vs)[kb, h]).max(1))[:, None]
+        o_tol[:, h] = (2.0 ** -11 + 2 * e)[:, None] * (p @ np.abs(V)) + lost + 2.0 ** -8 * np.abs(o)
         lse = np.where(live[:, 0], np.where(live, top, 0.0)[:, 0] + np.log(np.where(l > 0, l, 1.0))[:, 0], 0.0)
         l_tol[:, h] = e + 2.0 ** -22 * (np.abs(lse) + 1)
     return o_tol, l_tol

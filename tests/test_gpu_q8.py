@@ -758,3 +758,51 @@ def test_attn_q8_nan_values_reach_every_row_however_small_their_weight(d, A, spl
         assert np.isnan(got[:, 0, 9]).all(), b
         rest = np.delete(np.arange(d), 9)
         assert np.array_equal(got[..., rest], o[..., rest]) and np.array_equal(glse, lse)
+
+
+# per block of 128 keys: (log2 of V's scale or None for 0, the keys' logit in log2 units)
+SPREADS = {
+    "two empty blocks": [(0, 0)] * 2 + [(None, 0)] * 2 + [(0, 0)] * 8,
+    "empty beside 2^30": [(30, 0), (None, 0)] * 6,
+    "empty beside 2^30, reversed": [(None, 0), (30, 0)] * 6,
+    "one block 2^200 above the rest": [(-100, 0)] * 5 + [(100, 0)] + [(-100, 0)] * 6,
+    "the weight on small values, large ones first": [(100, -250)] + [(-100, 0)] * 11,
+    "the weight on small values, large ones last": [(-100, 0)] * 11 + [(100, -250)],
+    "large and small values that count alike": [(-100, 0), (100, -198)] * 6,
+    "the same, other way round": [(100, -198), (-100, 0)] * 6,
+    "the weight on empty blocks": [(None, 40)] * 6 + [(0, 0)] * 6,
+    "the weight on empty blocks behind": [(0, 0)] * 6 + [(None, 40)] * 6,
+    "a little weight on empty blocks": [(0, 0)] * 3 + [(None, -12)] * 9,
+    "half of the weight on a block 2^70 below": [(-40, 0), (30, 0)] * 6,
+    "steps of 2^50": [(-100 + 50 * (i % 5), -10 * (i % 3)) for i in range(12)],
+    "all empty": [(None, 3 * (i % 2)) for i in range(12)],
+    "all small": [(-100, i) for i in range(12)],
+    "all large": [(100, -i) for i in range(12)],
+}
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("A,masked", [(5, False), (16, False), (60, False), (128, False), (300, False), (300, True)])
+@pytest.mark.parametrize("name", list(SPREADS))
+def test_attn_q8_sums_hold_over_the_whole_range_of_value_scales(name, A, masked, d):
+    """Scales of V from 0 over 2^-100 to 2^100 in one head: a key counts in the sum whatever its V's scale is."""
+    H, N = 2, 12 * 128 - 5
+    rng = np.random.default_rng(7)
+    u, scale = rng.choice([-1.0, 1.0], d), 0.25
+    blocks = SPREADS[name]
+    at = np.array([x for _, x in blocks], float) * math.log(2) / (scale * d)
+    k = at[np.arange(N) // 128][:, None, None] * u + 0.02 * rng.standard_normal((N, H, d))
+    cache = [Q.kv_sync_q8(np.zeros((N, H, d)), np.zeros((12, H)), x, np.arange(N)) for x in (k, rng.standard_normal((N, H, d)))]
+    vs = np.array([0.0 if e is None else 2.0 ** e for e, _ in blocks])[:, None].repeat(H, 1)
+    cache[1] = (cache[1][0], vs)
+    q = torch.from_numpy(u + 0.02 * rng.standard_normal((A, H, d))).bfloat16()
+    idx = _idx(N, A, 3)
+    bm = np.ones((12, 12), np.uint8) if masked else None
+    kk, vv = _values(cache)
+    ref, rlse = O.pruned_attn(q, kk, vv, idx, scale, blockmask=bm)
+    ot, lt = Q.q8_attn_bound(q, kk, vv, vs, idx, scale, bm, floor=2.0 ** -25)
+    for ws in (None, torch.empty(0, dtype=torch.uint8, device=DEV)):
+        o, lse = _run_attn(cache, q, idx, scale, bm=bm, ws=None if masked else ws)
+        assert np.all(np.abs(lse - rlse) <= lt), float((np.abs(lse - rlse) / lt).max())
+        # bf16 and fp32 hold normal numbers down to 2^-126; what is smaller may become 0
+        assert np.all(np.abs(o - ref) <= ot + 2.0 ** -126), float((np.abs(o - ref) / ot).max())

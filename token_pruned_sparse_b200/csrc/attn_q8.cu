@@ -16,7 +16,8 @@
 //   one bf16 MMA costs, K stays 8 bits wide in shared memory, and no key is converted.
 // - ks_b enters as the factor of the exponent's FMA. vs_b enters as log2(vs_b) in its
 //   addend, so that P' = 2^(x + log2 vs_b - m) multiplies the codes of V directly; the row
-//   sum takes P' / vs_b. Neither costs an instruction per element.
+//   sum takes P' / vs_b, with a reference of its own (attn_q8.cuh). Neither costs an
+//   instruction per element, but in blocks whose vs_b is 0 or 2^60 below others'.
 // - P' V needs V as wide as P: four converter warps turn the codes into f16 (exact, e4m3 is
 //   a subset of f16) on the way from global to the swizzled shared tile. P' is f16: 11
 //   bits against bf16's 8 make its rounding (2^-11 per probability) vanish beside the
@@ -524,7 +525,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       barrier_softmax();                                        // s_rowc
     }
     const float rowc = works ? s_rowc[lrow] : 1.f;
-    float m_run = -INFINITY, l_run = 0.f;
+    float m_run = -INFINITY, s_run = -INFINITY, l_run = 0.f;   // references of P' and O, and of the sum
     bool ok = true;
     const int nsteps = steps(t);
     auto scales = [&](int j, float& ks, float& vs) {
@@ -536,8 +537,8 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     if (works && nsteps > 0) scales(0, ks_next, vs_next);
     for (int j = 0; works && j < nsteps; ++j) {
       const float c = fmaxf(rowc * ks_next, kFactorMin);
-      const float vs = fminf(fmaxf(vs_next, kScaleMin), kScaleMax);
-      const float lv = __log2f(vs), ivs = 1.f / vs;
+      const float lv = log2_scale(vs_next);
+      float share = share_of(m_run, lv, s_run);
       if (j + 1 < nsteps) scales(j + 1, ks_next, vs_next);
       const int64_t key0 = static_cast<int64_t>(key_tile(seq(t, j))) * kBN;
       const int nvalid = static_cast<int>(p.N - key0 < kBN ? p.N - key0 : kBN);
@@ -577,7 +578,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
           tmem_ld32_end(s1);
           exp_cols_f16(s1, c2, nb2, pk + 16, acc);
           lt = sum();
-          slow = __any_sync(0xffffffffu, !(lt <= kSumLimit));
+          slow = __any_sync(0xffffffffu, !(lt <= kSumLimit && share <= kShareMax));
         }
         if (slow) {                                 // S is intact: P' of this half has not been stored yet
           uint32_t sr[64];
@@ -591,8 +592,12 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 #pragma unroll
           for (int i = 0; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(sr[i]));
           // a tile's first half has a key below N, so the first maximum is finite (or S is NaN, and so is
-          // the row)
-          const float m_new = fmaxf(m_run, fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), c, lv));
+          // the row); m stays -inf until a key has a value
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+          const float m_new = fmaxf(m_run, top + lv);
+          const float s_new = fmaxf(s_run, top);
+          l_run *= fast_exp2(s_run - s_new);
+          s_run = s_new;
           if (j == 0 && u == 0) {
             m_run = m_new;
           } else if (__any_sync(0xffffffffu, m_new > m_run)) {
@@ -611,18 +616,33 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
               for (int i = 0; i < 16; ++i) o[i] *= alpha;
               tmem_st16(tO(t) + lane_off + i0, o);
             }
-            l_run *= alpha;
             m_run = m_new;
           }
-          const uint64_t nb2 = f2_pack(lv - m_run, lv - m_run);
-          acc[0] = acc[1] = f2_pack(0.f, 0.f);
           uint32_t(&lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(sr);
           uint32_t(&hi)[32] = *reinterpret_cast<uint32_t(*)[32]>(sr + 32);
-          exp_cols_f16(lo, c2, nb2, pk, acc);
-          exp_cols_f16(hi, c2, nb2, pk + 16, acc);
-          lt = sum();
+          auto exponentials = [&](float base) {
+            const uint64_t nb2 = f2_pack(base, base);
+            acc[0] = acc[1] = f2_pack(0.f, 0.f);
+            exp_cols_f16(lo, c2, nb2, pk, acc);
+            exp_cols_f16(hi, c2, nb2, pk + 16, acc);
+            lt = sum();
+          };
+          share = share_of(m_run, lv, s_run);
+          const bool alone = __any_sync(0xffffffffu, !(share <= kShareMax));
+          if (alone) {
+            exponentials(-s_run);
+            l_run += lt;
+          }
+          if (lv == -INFINITY) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) pk[i] = 0u;
+          } else {
+            exponentials(lv - m_run);
+          }
+          if (!alone) l_run = fmaf(lt, share, l_run);
+        } else {
+          l_run = fmaf(lt, share, l_run);
         }
-        l_run = fmaf(lt, ivs, l_run);
         tmem_st32_words(at, pk);                    // P' over S columns that have been read
         tc_fence_before();
         mbar_arrive(bar(L::p_full + 2 * t + u));
@@ -633,7 +653,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     if (ok && nsteps > 0) ok = mbar_wait(bar(L::o_full + t), 0, &s_abort, prm.status);
     ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
-    float w0 = 1.f, w1 = 0.f;                     // weights of this tile's and the other tile's sums
+    float w1 = 0.f;
     constexpr int kMine = kOneSet ? D / 2 : D;    // columns of the output that this thread writes, from c0
     const int c0 = kOneSet ? t * kMine : 0;
     const float* other = nullptr;
@@ -642,9 +662,9 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       // products are complete), chunks rotated by row so the 16-byte accesses of a warp hit distinct banks.
       // With shifted lanes the two threads of a row sit in different warps: both have r.
       float4* stage = reinterpret_cast<float4*>(gbase + L::kV);
-      float2* s_ml = reinterpret_cast<float2*>(gbase + L::kList);   // [tile][row]; the list is done with
+      float4* s_msl = reinterpret_cast<float4*>(gbase + L::kList);   // [tile][row]; the list is done with
       barrier_softmax();
-      s_ml[t * kBM + r] = make_float2(m_run, l_run);
+      s_msl[t * kBM + r] = make_float4(m_run, s_run, l_run, 0.f);
       if (ok && works && nsteps > 0) {
 #pragma unroll
         for (int i0 = 0; i0 < kMine; i0 += 32) {
@@ -658,20 +678,19 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       }
       barrier_softmax();
       ok = __all_sync(0xffffffffu, ok && !s_abort);
-      const float2 ml = s_ml[(1 - t) * kBM + r];
-      const float m = fmaxf(m_run, ml.x);
-      w0 = part_weight(m_run, l_run, m);
-      w1 = part_weight(ml.x, ml.y, m);
-      l_run = (w0 != 0.f ? w0 * l_run : 0.f) + (w1 != 0.f ? w1 * ml.y : 0.f);
-      m_run = m;
+      const float4 msl = s_msl[(1 - t) * kBM + r];
+      const float s = fmaxf(s_run, msl.y);
+      l_run = part_weight(s_run, l_run, s) * l_run + part_weight(msl.y, msl.z, s) * msl.z;
+      s_run = s;
+      w1 = value_weight(msl.x, s);
       other = reinterpret_cast<const float*>(stage + (1 - t) * kBM * kChunks);
     }
     if (!ok || !works) return;
     // a row with no key has l = 0: o = 0, lse = -inf; a NaN sum stays NaN
     const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
-    w0 *= inv;
+    const float w0 = value_weight(m_run, s_run) * inv;   // weights of this tile's and the other tile's O
     w1 *= inv;
-    const float lse = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
+    const float lse = l_run == 0.f ? -INFINITY : (s_run + log2f(l_run)) * kLn2;
     const int64_t orow = row * p.H + h;
     const int64_t prow = prm.nsplit > 1 ? static_cast<int64_t>(blockIdx.z) * prm.part_rows * p.H + orow - prm.part_row0 * p.H : 0;
 #pragma unroll
@@ -682,7 +701,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 #pragma unroll
       for (int i = 0; i < 32; ++i) o[i] = nsteps > 0 ? o[i] * w0 : 0.f;   // (a weight of 0 keeps a NaN of V)
       if constexpr (kOneSet) {
-        if (steps(1 - t) > 0) {
+        if (ntiles > 1 - t) {                     // the other tile has steps
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             const float4 x = reinterpret_cast<const float4*>(other)[r * kChunks + (i0 / 4 + q + r) % kChunks];

@@ -20,15 +20,32 @@ struct Q8Args {
   unsigned int* status;
 };
 
-// A scale of 0 (an empty block) stands for values of 0: the smallest positive factors give just that.
+// A key scale of 0 (an empty block) stands for logits of 0: the smallest positive factor gives just that.
 constexpr float kFactorMin = 1.17549435e-38f;
 constexpr float kScaleMin = 7.8886091e-31f, kScaleMax = 1.2676506e30f;   // 2^-100, 2^100
 
-// Weight of a partial result with maximum m_part (log2) and sum l_part against the maximum m of all: 0 without a
-// key, NaN where the sum is NaN (its maximum may then be -inf).
-__device__ __forceinline__ float part_weight(float m_part, float l_part, float m) {
+// A row has two references (log2): m of x + log2 vs, which P' and O count in, and s of x, which the sum l counts in
+// (the largest values when they were set). A key's share of the sum is P' 2^(m - log2 vs - s). Up to kShareMax of that
+// factor a P' that underflows (2^-126) is of a key below 2^-66 of the sum. Beyond it (blocks whose vs is far below
+// others'), and where vs is 0 (values of 0: P' = 0), a second pass of exponentials takes the sum.
+constexpr float kShareMax = 1.1529215e18f;   // 2^60
+__device__ __forceinline__ float share_of(float m, float lv, float s) {
+  return fminf(fast_exp2(m - lv - s), 3e38f);   // finite: it may meet sums of 0 (NaN, without references yet: 3e38)
+}
+// log2 of a V scale; -inf for 0, and for a negative or NaN one, which counts as 0
+__device__ __forceinline__ float log2_scale(float vs) {
+  return vs > 0.f ? __log2f(fminf(fmaxf(vs, kScaleMin), kScaleMax)) : -INFINITY;
+}
+
+// Weight of a partial sum l_part in units of 2^s_part in one of 2^s: 0 without a key, NaN where the sum is NaN (its
+// reference may then be -inf).
+__device__ __forceinline__ float part_weight(float s_part, float l_part, float s) {
   if (l_part != l_part) return l_part;
-  return m_part == -INFINITY ? 0.f : fast_exp2(m_part - m);
+  return s_part == -INFINITY ? 0.f : fast_exp2(s_part - s);
+}
+// Weight of a partial O in units of 2^m_part against sums in units of 2^s: 0 if it has no key with a value.
+__device__ __forceinline__ float value_weight(float m_part, float s) {
+  return m_part == -INFINITY ? 0.f : fast_exp2(m_part - s);
 }
 
 // At most kFewRows rows of a dense call (attn_q8_few.cu).

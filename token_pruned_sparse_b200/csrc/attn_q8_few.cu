@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kThreads, few_ctas(kSets)) attn_q8_few_kernel(
   constexpr int kKV = D / 64;           // 16-byte vectors of a thread's key (4 threads hold D channels)
   constexpr int kVW = D / 32;           // words of a thread's V channels (D / 8 of them) of one key
   __shared__ float s_o[kWarps][8 * kSets][D + 4];
-  __shared__ float2 s_ml[kWarps][8 * kSets];
+  __shared__ float4 s_msl[kWarps][8 * kSets];
 
   const AttnArgs& p = prm.a;
   const int rows = static_cast<int>(active_count(p.count, p.cap));
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, few_ctas(kSets)) attn_q8_few_kernel(
     for (int i = 0; i < kTilesM; ++i)
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[e][i][k] = 0.f;
-  float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+  float m_run[2] = {-INFINITY, -INFINITY}, s_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
 
   // codes of 16 keys: K of keys g and g + 8 (channels 64 v + 16 t ..), V of keys 2t, 2t + 1, 2t + 8, 2t + 9
   // (channels g D / 8 ..)
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, few_ctas(kSets)) attn_q8_few_kernel(
     }
   };
 
-  auto step = [&](const Codes& c, int64_t key0, const float (&cc)[2], float lv, float ivs) {
+  auto step = [&](const Codes& c, int64_t key0, const float (&cc)[2], float lv, float (&share)[kSets]) {
     // ---- S = Q K^T: sf[n] = rows g, g + 8 x keys 8 n + 2t, 8 n + 2t + 1 -----------------------------
     // (even and odd steps apart: the four chains of products are half as long)
     float sf[2][4], sg[2][4];
@@ -211,20 +211,23 @@ __global__ void __launch_bounds__(kThreads, few_ctas(kSets)) attn_q8_few_kernel(
     probabilities();                   // (no reference yet: sums are +inf)
     bool outgrown = !whole;
 #pragma unroll
-    for (int e = 0; e < kSets; ++e) outgrown = outgrown || !(lt[e] <= kSumLimit);
+    for (int e = 0; e < kSets; ++e) outgrown = outgrown || !(lt[e] <= kSumLimit && share[e] <= kShareMax);
     if (__any_sync(0xffffffffu, outgrown)) {
-      float alpha[kSets];
 #pragma unroll
       for (int e = 0; e < kSets; ++e) {
         float mx = fmaxf(fmaxf(sf[0][2 * e], sf[0][2 * e + 1]), fmaxf(sf[1][2 * e], sf[1][2 * e + 1]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // a step has a key below N, so the maximum is finite (or S is NaN, and so is the row)
-        const float m_new = fmaxf(m_run[e], fmaf(mx, cc[e], lv));
-        alpha[e] = m_run[e] == -INFINITY ? 0.f : fast_exp2(m_run[e] - m_new);
+        // a step has a key below N, so the maximum is finite (or S is NaN, and so is the row); m stays -inf
+        // until a key has a value
+        mx *= cc[e];
+        const float m_new = fmaxf(m_run[e], mx + lv), s_new = fmaxf(s_run[e], mx);
+        const float alpha = m_run[e] == -INFINITY ? 0.f : fast_exp2(m_run[e] - m_new);
         m_run[e] = m_new;
-        l_run[e] *= alpha[e];
-        const float a0 = __shfl_sync(0xffffffffu, alpha[e], 8 * t), a1 = __shfl_sync(0xffffffffu, alpha[e], 8 * t + 4);
+        l_run[e] *= fast_exp2(s_run[e] - s_new);
+        s_run[e] = s_new;
+        share[e] = share_of(m_new, lv, s_new);
+        const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * t), a1 = __shfl_sync(0xffffffffu, alpha, 8 * t + 4);
 #pragma unroll
         for (int i = 0; i < kTilesM; ++i) {    // O^T holds rows 2t and 2t + 1
           o[e][i][0] *= a0;
@@ -234,12 +237,30 @@ __global__ void __launch_bounds__(kThreads, few_ctas(kSets)) attn_q8_few_kernel(
         }
       }
       probabilities();
+      bool alone = false;
+#pragma unroll
+      for (int e = 0; e < kSets; ++e) alone = alone || !(share[e] <= kShareMax);
+      if (__any_sync(0xffffffffu, alone)) {
+#pragma unroll
+        for (int e = 0; e < kSets; ++e) {
+          float sum = 0.f;
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              sum += fast_exp2(fmaf(sf[n][2 * e + k], cc[e], -s_run[e]));
+              if (lv == -INFINITY) pf[e][2 * n + k] = 0.f;
+            }
+          l_run[e] += sum;
+          lt[e] = 0.f;
+        }
+      }
     }
     // ---- O^T += V^T P'^T ---------------------------------------------------------------------------------
     uint32_t pb[kSets][2];
 #pragma unroll
     for (int e = 0; e < kSets; ++e) {
-      l_run[e] = fmaf(lt[e], ivs, l_run[e]);
+      l_run[e] = fmaf(lt[e], share[e], l_run[e]);
       pb[e][0] = pack_f16x2(pf[e][0], pf[e][1]);
       pb[e][1] = pack_f16x2(pf[e][2], pf[e][3]);
     }
@@ -269,8 +290,10 @@ __global__ void __launch_bounds__(kThreads, few_ctas(kSets)) attn_q8_few_kernel(
   for (int b = first; b < b1; b += kWarps) {
     const int64_t at = static_cast<int64_t>(b) * p.H + h;
     const float ks = __ldg(prm.ks + at);
-    const float vs = fminf(fmaxf(__ldg(prm.vs + at), kScaleMin), kScaleMax);
-    const float lv = __log2f(vs), ivs = 1.f / vs;
+    const float lv = log2_scale(__ldg(prm.vs + at));
+    float share[kSets];
+#pragma unroll
+    for (int e = 0; e < kSets; ++e) share[e] = share_of(m_run[e], lv, s_run[e]);
     const float cc[2] = {fmaxf(rowc[0] * ks, kFactorMin), fmaxf(rowc[1] * ks, kFactorMin)};
     const int64_t key0 = static_cast<int64_t>(b) * kScaleBlock;
     const int nstep = static_cast<int>(((p.N - key0 < kScaleBlock ? p.N - key0 : kScaleBlock) + kKeys - 1) / kKeys);
@@ -279,9 +302,9 @@ __global__ void __launch_bounds__(kThreads, few_ctas(kSets)) attn_q8_few_kernel(
     for (int i = 0; i < nstep; i += 2) {       // two steps, so that the two buffers keep their registers
       const int64_t k0 = key0 + i * kKeys;
       load(buf[1], i + 1 < nstep ? k0 + kKeys : p.N);
-      step(buf[0], k0, cc, lv, ivs);
+      step(buf[0], k0, cc, lv, share);
       load(buf[0], i + 2 < nstep ? k0 + 2 * kKeys : next_block);
-      if (i + 1 < nstep) step(buf[1], k0 + kKeys, cc, lv, ivs);
+      if (i + 1 < nstep) step(buf[1], k0 + kKeys, cc, lv, share);
     }
   }
 
@@ -291,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, few_ctas(kSets)) attn_q8_few_kernel(
     float l = l_run[e];
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
-    if (t == 0) s_ml[warp][8 * e + g] = make_float2(m_run[e], l);
+    if (t == 0) s_msl[warp][8 * e + g] = make_float4(m_run[e], s_run[e], l, 0.f);
 #pragma unroll
     for (int i = 0; i < kTilesM; ++i) {
       const int ch = g * (D / 8) + 2 * i;
@@ -302,32 +325,31 @@ __global__ void __launch_bounds__(kThreads, few_ctas(kSets)) attn_q8_few_kernel(
   __syncthreads();
   for (int i = tid; i < rows * (D / 4); i += kThreads) {
     const int r = i / (D / 4), c4 = i % (D / 4);
-    float m = -INFINITY;
+    float ref = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_ml[w][r].x);
-    float l = 0.f;
+    for (int w = 0; w < kWarps; ++w) ref = fmaxf(ref, s_msl[w][r].y);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) l = fmaf(part_weight(s_msl[w][r].y, s_msl[w][r].z, ref), s_msl[w][r].z, l);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float2 ml = s_ml[w][r];
-      const float f = part_weight(ml.x, ml.y, m);        // (a weight of 0 keeps a NaN of V)
+      const float f = value_weight(s_msl[w][r].x, ref) * inv;   // (a weight of 0 keeps a NaN of V)
       const float4 x = *reinterpret_cast<const float4*>(&s_o[w][r][4 * c4]);
       a.x = fmaf(f, x.x, a.x);
       a.y = fmaf(f, x.y, a.y);
       a.z = fmaf(f, x.z, a.z);
       a.w = fmaf(f, x.w, a.w);
-      l = fmaf(f, ml.y, l);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    const float lse = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
     const int64_t orow = static_cast<int64_t>(r) * p.H + h;
     if (gridDim.y > 1) {
       const int64_t prow = static_cast<int64_t>(blockIdx.y) * prm.part_rows * p.H + orow;
-      reinterpret_cast<float4*>(prm.o_part + prow * D)[c4] = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+      reinterpret_cast<float4*>(prm.o_part + prow * D)[c4] = a;
       if (c4 == 0) prm.lse_part[prow] = lse;
     } else {
       reinterpret_cast<uint2*>(p.o + orow * D)[c4] =
-          make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+          make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
       if (c4 == 0 && p.lse) p.lse[orow] = lse;
     }
   }
