@@ -806,3 +806,33 @@ def test_attn_q8_sums_hold_over_the_whole_range_of_value_scales(name, A, masked,
         assert np.all(np.abs(lse - rlse) <= lt), float((np.abs(lse - rlse) / lt).max())
         # bf16 and fp32 hold normal numbers down to 2^-126; what is smaller may become 0
         assert np.all(np.abs(o - ref) <= ot + 2.0 ** -126), float((np.abs(o - ref) / ot).max())
+
+
+def _one_loud_key(A, d, loud, ws):
+    """A million keys at 2^-26 of the weight of key `loud` hold 1.5% of the sum. Their values are 1, its values 0.
+    Returns (o, lse), the exact ones, and q8_attn_bound's bound e of a logit."""
+    N, H, scale = 1 << 20, 1, 0.25
+    codes = [torch.zeros((N, H, d), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    sc = [torch.full((N // 128, H), 2.0 ** -8, device=DEV) for _ in range(2)]
+    codes[1][:] = 0x78                                               # 256: values of 1
+    codes[1][loud] = 0                                               # and 0 under the large weight
+    u = np.random.default_rng(1).choice([-1.0, 1.0], d)
+    codes[0][loud, 0] = Q.codes_of(256.0 * u)
+    assert Q.e4m3_decode([0x78])[0] == 256.0
+    at = 26.0 * math.log(2) / (scale * d)                            # the logit in log2 units is 26
+    q = torch.from_numpy(np.broadcast_to(at * u, (A, H, d)).copy()).bfloat16()
+    x = float((O.f64(q[0, 0]) * u).sum() * scale)
+    total = math.exp(x) + (N - 1)
+    e = scale * (2.0 ** -17 * at * d + 2 * d * 2.0 ** -23 * at * d) + 2.0 ** -22 * (x * math.log2(math.e) + 4)
+    ws = None if ws else torch.empty(0, dtype=torch.uint8, device=DEV)
+    return _run_attn(None, q, np.arange(A, dtype=np.int32), scale, ws=ws, dev=(*codes, *sc)), ((N - 1) / total, math.log(total)), e
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("A", [5, 16, 60, 300])
+@pytest.mark.parametrize("loud", [3, (1 << 20) - 9])
+@pytest.mark.parametrize("split", [False, True])
+def test_attn_q8_a_long_sum_loses_no_small_terms(A, d, loud, split):
+    """16,384 additions of 2^-24 to a sum of 1: rounded one by one, fp32 would drop them all (lse off by 2^-10)."""
+    (_, lse), (_, rlse), e = _one_loud_key(A, d, loud, split)
+    assert np.abs(lse - rlse).max() <= e + 2.0 ** -22 * (rlse + 1)

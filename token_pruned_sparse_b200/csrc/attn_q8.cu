@@ -526,6 +526,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     }
     const float rowc = works ? s_rowc[lrow] : 1.f;
     float m_run = -INFINITY, s_run = -INFINITY, l_run = 0.f;   // references of P' and O, and of the sum
+    float l_low = 0.f;                            // what l_run's additions rounded off
     bool ok = true;
     const int nsteps = steps(t);
     auto scales = [&](int j, float& ks, float& vs) {
@@ -596,7 +597,9 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
           const float m_new = fmaxf(m_run, top + lv);
           const float s_new = fmaxf(s_run, top);
-          l_run *= fast_exp2(s_run - s_new);
+          const float beta = fast_exp2(s_run - s_new);
+          l_run *= beta;
+          l_low *= beta;
           s_run = s_new;
           if (j == 0 && u == 0) {
             m_run = m_new;
@@ -631,7 +634,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
           const bool alone = __any_sync(0xffffffffu, !(share <= kShareMax));
           if (alone) {
             exponentials(-s_run);
-            l_run += lt;
+            add_low(l_low + lt, l_run, l_low);
           }
           if (lv == -INFINITY) {
 #pragma unroll
@@ -639,9 +642,9 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
           } else {
             exponentials(lv - m_run);
           }
-          if (!alone) l_run = fmaf(lt, share, l_run);
+          if (!alone) add_low(fmaf(lt, share, l_low), l_run, l_low);
         } else {
-          l_run = fmaf(lt, share, l_run);
+          add_low(fmaf(lt, share, l_low), l_run, l_low);
         }
         tmem_st32_words(at, pk);                    // P' over S columns that have been read
         tc_fence_before();

@@ -37,6 +37,13 @@ __device__ __forceinline__ float log2_scale(float vs) {
   return vs > 0.f ? __log2f(fminf(fmaxf(vs, kScaleMin), kScaleMax)) : -INFINITY;
 }
 
+// l += y, with what the addition rounds off (of y, which takes in the last such rest) kept in low
+__device__ __forceinline__ void add_low(float y, float& l, float& low) {
+  const float t = l + y;
+  low = y - (t - l);
+  l = t;
+}
+
 // Weight of a partial sum l_part in units of 2^s_part in one of 2^s: 0 without a key, NaN where the sum is NaN (its
 // reference may then be -inf).
 __device__ __forceinline__ float part_weight(float s_part, float l_part, float s) {

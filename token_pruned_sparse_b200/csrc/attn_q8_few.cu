@@ -126,6 +126,7 @@ __global__ void __launch_bounds__(kThreads, few_ctas(kSets)) attn_q8_few_kernel(
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[e][i][k] = 0.f;
   float m_run[2] = {-INFINITY, -INFINITY}, s_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+  float l_low[2] = {0.f, 0.f};           // what l_run's additions rounded off
 
   // codes of 16 keys: K of keys g and g + 8 (channels 64 v + 16 t ..), V of keys 2t, 2t + 1, 2t + 8, 2t + 9
   // (channels g D / 8 ..)
@@ -224,7 +225,9 @@ __global__ void __launch_bounds__(kThreads, few_ctas(kSets)) attn_q8_few_kernel(
         const float m_new = fmaxf(m_run[e], mx + lv), s_new = fmaxf(s_run[e], mx);
         const float alpha = m_run[e] == -INFINITY ? 0.f : fast_exp2(m_run[e] - m_new);
         m_run[e] = m_new;
-        l_run[e] *= fast_exp2(s_run[e] - s_new);
+        const float beta = fast_exp2(s_run[e] - s_new);
+        l_run[e] *= beta;
+        l_low[e] *= beta;
         s_run[e] = s_new;
         share[e] = share_of(m_new, lv, s_new);
         const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * t), a1 = __shfl_sync(0xffffffffu, alpha, 8 * t + 4);
@@ -251,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, few_ctas(kSets)) attn_q8_few_kernel(
               sum += fast_exp2(fmaf(sf[n][2 * e + k], cc[e], -s_run[e]));
               if (lv == -INFINITY) pf[e][2 * n + k] = 0.f;
             }
-          l_run[e] += sum;
+          add_low(l_low[e] + sum, l_run[e], l_low[e]);
           lt[e] = 0.f;
         }
       }
@@ -260,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, few_ctas(kSets)) attn_q8_few_kernel(
     uint32_t pb[kSets][2];
 #pragma unroll
     for (int e = 0; e < kSets; ++e) {
-      l_run[e] = fmaf(lt[e], share[e], l_run[e]);
+      add_low(fmaf(lt[e], share[e], l_low[e]), l_run[e], l_low[e]);
       pb[e][0] = pack_f16x2(pf[e][0], pf[e][1]);
       pb[e][1] = pack_f16x2(pf[e][2], pf[e][3]);
     }
