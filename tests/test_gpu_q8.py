@@ -836,3 +836,15 @@ def test_attn_q8_a_long_sum_loses_no_small_terms(A, d, loud, split):
     """16,384 additions of 2^-24 to a sum of 1: rounded one by one, fp32 would drop them all (lse off by 2^-10)."""
     (_, lse), (_, rlse), e = _one_loud_key(A, d, loud, split)
     assert np.abs(lse - rlse).max() <= e + 2.0 ** -22 * (rlse + 1)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("A", [5, 16, 60, 300])
+@pytest.mark.parametrize("loud", [3, (1 << 20) - 9])
+@pytest.mark.parametrize("split", [False, True])
+def test_attn_q8_many_small_weights_count_beside_a_large_one(A, d, loud, split):
+    """As above: the values under the small weights must not get lost in f16."""
+    (o, _), (ref, _), e = _one_loud_key(A, d, loud, split)
+    # as q8_attn_bound: f16's normal rounding, e twice, bf16, and N 2^-33 of the largest p vs by 448
+    tol = (2.0 ** -11 + 2 * e + 2.0 ** -8) * ref + 2.0 ** 20 * 2.0 ** -33 * 448 * 2.0 ** -8
+    assert np.abs(o - ref).max() <= tol, (float(np.abs(o - ref).max()), tol, ref)

@@ -24,10 +24,13 @@ struct Q8Args {
 constexpr float kFactorMin = 1.17549435e-38f;
 constexpr float kScaleMin = 7.8886091e-31f, kScaleMax = 1.2676506e30f;   // 2^-100, 2^100
 
-// A row has two references (log2): m of x + log2 vs, which P' and O count in, and s of x, which the sum l counts in
-// (the largest values when they were set). A key's share of the sum is P' 2^(m - log2 vs - s). Up to kShareMax of that
+// A row has two references (log2): m, the largest x + log2 vs less kRaise, which P' and O count in, and s, the largest
+// x, which the sum l counts in (the largest when they were set). With kRaise the largest P' is 2^8 or more and f16's
+// subnormals end at 2^-33 of it: what a cache of N keys can lose is N 2^-33 of its largest term. With P' <= 1 it was
+// N 2^-25, 3% at a million keys. A key's share of the sum is P' 2^(m - log2 vs - s). Up to kShareMax of that
 // factor a P' that underflows (2^-126) is of a key below 2^-66 of the sum. Beyond it (blocks whose vs is far below
 // others'), and where vs is 0 (values of 0: P' = 0), a second pass of exponentials takes the sum.
+constexpr float kRaise = 8.f;
 constexpr float kShareMax = 1.1529215e18f;   // 2^60
 __device__ __forceinline__ float share_of(float m, float lv, float s) {
   return fminf(fast_exp2(m - lv - s), 3e38f);   // finite: it may meet sums of 0 (NaN, without references yet: 3e38)

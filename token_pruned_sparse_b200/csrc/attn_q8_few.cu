@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, few_ctas(kSets)) attn_q8_few_kernel(
         // a step has a key below N, so the maximum is finite (or S is NaN, and so is the row); m stays -inf
         // until a key has a value
         mx *= cc[e];
-        const float m_new = fmaxf(m_run[e], mx + lv), s_new = fmaxf(s_run[e], mx);
+        const float m_new = fmaxf(m_run[e], mx + (lv - kRaise)), s_new = fmaxf(s_run[e], mx);
         const float alpha = m_run[e] == -INFINITY ? 0.f : fast_exp2(m_run[e] - m_new);
         m_run[e] = m_new;
         const float beta = fast_exp2(s_run[e] - s_new);
