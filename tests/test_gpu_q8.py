@@ -848,3 +848,17 @@ def test_attn_q8_many_small_weights_count_beside_a_large_one(A, d, loud, split):
     # as q8_attn_bound: f16's normal rounding, e twice, bf16, and N 2^-33 of the largest p vs by 448
     tol = (2.0 ** -11 + 2 * e + 2.0 ** -8) * ref + 2.0 ** 20 * 2.0 ** -33 * 448 * 2.0 ** -8
     assert np.abs(o - ref).max() <= tol, (float(np.abs(o - ref).max()), tol, ref)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("A", [5, 60, 300])
+@pytest.mark.parametrize("power", [-115, -104, 104, 112, 125])
+def test_attn_q8_queries_at_the_ends_of_bf16(A, d, power):
+    """Rows of Q of 2^power, with a softmax scale that makes their logits ordinary ones."""
+    N, H = 700, 2
+    cache, q, idx = _attn_case(N, A, H, d, 37)
+    q = (q.double().clamp(-3.5, 3.5) * 2.0 ** power).bfloat16()
+    assert bool(q.isfinite().all())
+    scale = 2.0 ** -power / math.sqrt(d)
+    o, lse = _run_attn(cache, q, idx, scale)
+    _check_attn(o, lse, cache, q, idx, scale)

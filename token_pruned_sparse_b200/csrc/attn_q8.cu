@@ -498,8 +498,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             if (fabsf(f[c]) < INFINITY) top = fmaxf(top, fabsf(f[c]));
 #pragma unroll
           for (int o = kLanesQ / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          float sc = scale_of_amax(top);
-          if (sc == 0.f) sc = 1.f;
+          const float sc = scale_of_row(top);
           const float inv = 1.f / sc;
           uint32_t hi[2], lo[2];
 #pragma unroll

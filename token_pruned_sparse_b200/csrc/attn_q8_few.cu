@@ -97,8 +97,7 @@ __global__ void __launch_bounds__(kThreads, few_ctas(kSets)) attn_q8_few_kernel(
     }
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    float sc = scale_of_amax(top);
-    if (sc == 0.f) sc = 1.f;
+    const float sc = scale_of_row(top);
     rowc[r] = prm.scale_log2 * sc;
     const float inv = 1.f / sc;
 #pragma unroll

@@ -35,12 +35,16 @@ __device__ __forceinline__ float2 f16x2_to_f2(uint32_t w) {
 // The smallest 2^e (as fp32) with amax <= 448 * 2^e, e kept in [-100, 100]; 0 for
 // amax = 0. 448 = 1.75 * 2^8, so with amax = 1.f * 2^E, e = E - 8 if 1.f <= 1.75
 // and E - 7 otherwise: exponent and mantissa bits decide, nothing is rounded.
+template <int kLeast = -100, int kMost = 100>
 __device__ __forceinline__ float scale_of_amax(float amax) {
   if (!(amax > 0.f)) return 0.f;
   const uint32_t b = __float_as_uint(amax);
   int e = static_cast<int>(b >> 23) - 127 - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  e = e < -100 ? -100 : (e > 100 ? 100 : e);
+  e = e < kLeast ? kLeast : (e > kMost ? kMost : e);
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
+// The power of two of a row of Q: as above over all of bf16 (the largest needs 2^120; rows below 448 * 2^-126
+// keep fewer bits), and 1 for a row of zeros.
+__device__ __forceinline__ float scale_of_row(float amax) { return amax > 0.f ? scale_of_amax<-126, 120>(amax) : 1.f; }
 
 }  // namespace tps
