@@ -862,3 +862,15 @@ def test_attn_q8_queries_at_the_ends_of_bf16(A, d, power):
     scale = 2.0 ** -power / math.sqrt(d)
     o, lse = _run_attn(cache, q, idx, scale)
     _check_attn(o, lse, cache, q, idx, scale)
+
+
+def test_attn_q8_takes_its_scale_as_pruned_attn_does():
+    """Whatever converts to a float, a zero-dimensional tensor among it."""
+    cache, q, idx = _attn_case(300, 20, 2, 64, 3)
+    q, cache, idx = q.to(DEV), _to_dev(cache), _dev(idx)
+    want = tps.pruned_attn_q8(q, *cache, *idx, 0.125)
+    kv = torch.zeros((300, 2, 64), dtype=torch.bfloat16, device=DEV)
+    for scale in (torch.tensor(0.125), np.float32(0.125), torch.tensor(0.125, device=DEV)):
+        tps.pruned_attn(q, kv, kv, *idx, scale)
+        assert torch.equal(tps.pruned_attn_q8(q, *cache, *idx, scale), want)
+    tps.tps_check()

@@ -559,8 +559,8 @@ def pruned_attn_q8(q_act, k_cache, v_cache, k_scale, v_scale, idx, count, scale,
             made.append(ws)
     if made:
         _made_for(stream, dev, *made)
-    _call(lib().pruned_attn_q8, dev, stream, a_q, a_kc, a_vc, a_ks, a_vs, a_idx, a_cnt, cap, N, H, d, scale, a_mask,
-          block, a_o, a_lse, a_ws, n_ws)
+    _call(lib().pruned_attn_q8, dev, stream, a_q, a_kc, a_vc, a_ks, a_vs, a_idx, a_cnt, cap, N, H, d, float(scale), a_mask,
+          int(block), a_o, a_lse, a_ws, n_ws)
     return o_act
 
 
