@@ -57,7 +57,8 @@ __global__ void __launch_bounds__(kThreads, few_ctas(kSets)) attn_q8_few_kernel(
   constexpr int kTilesM = D / 16;       // 16-channel tiles of O^T
   constexpr int kKV = D / 64;           // 16-byte vectors of a thread's key (4 threads hold D channels)
   constexpr int kVW = D / 32;           // words of a thread's V channels (D / 8 of them) of one key
-  __shared__ float s_o[kWarps][8 * kSets][D + 4];
+  __shared__ __align__(16) float s_o[kWarps][8 * kSets][D + 4];   // written 8 bytes, read 16 bytes at a time
+  static_assert((D + 4) * sizeof(float) % 16 == 0, "rows of s_o keep its alignment");
   __shared__ float4 s_msl[kWarps][8 * kSets];
 
   const AttnArgs& p = prm.a;
