@@ -427,7 +427,8 @@ TPS_API int pruned_attn_mma(const tps_bf16* q_act, const tps_bf16* k, const tps_
  * ws: device memory of tps_attn_q8_workspace_size(cap, N, H, d) bytes (0 when no key
  * split is chosen), 16-byte aligned, no initialisation: a dense call whose grid would
  * leave the GPU partly idle (few active rows, or a mostly empty last wave) runs as
- * S <= 32 key ranges there, merged by a second launch. With a NULL or smaller
+ * several key ranges there, merged by a last launch (up to 64 ranges, 128 with cap <= 16;
+ * ask the function, the number is not to be derived). With a NULL or smaller
  * workspace the call runs unsplit. Calls that share a workspace must be ordered
  * on the GPU. d in {64, 128}; 1 <= H <= 256; N, cap < 2^31. */
 TPS_API int pruned_attn_q8(const tps_bf16* q_act, const uint8_t* k_cache, const uint8_t* v_cache,
