@@ -419,11 +419,13 @@ TPS_API int pruned_attn_mma(const tps_bf16* q_act, const tps_bf16* k, const tps_
  * 128, are left as they were and flagged (TPS_ERR_BOUNDS at tps_check). Without a mask idx
  * is not read. Rows j >= min(*count, cap) of o_act and lse are left as they were. Scales must be finite
  * and >= 0 (a scale of 0 stands for values of 0), the non-zero v_scale within
- * [2^-100, 2^100]. The codes are used as they are: Q enters the e4m3 products as two
- * e4m3 parts (exact for channels down to 2^-10 of a row's largest), the
- * probabilities and V's codes meet in f16, sums are fp32. Key blocks that a mask
- * leaves out are not read. A NaN code in an attended block makes the rows that
- * attend it NaN.
+ * [2^-100, 2^100], in any ratio to each other. The codes are used as they are: Q enters
+ * the e4m3 products as two e4m3 parts (exact for channels down to 2^-9 of a row's
+ * largest, within 2^-17 of the largest below that; a row whose largest is below 2^-117
+ * keeps fewer bits), the probabilities and V's codes meet in f16 (a key's weight times its
+ * v_scale may vanish below 2^-33 of the row's largest), sums are fp32. Key blocks
+ * that a mask leaves out are not read, nor are their scales. A NaN code of K in an attended
+ * block makes the rows that attend it NaN, one of V its channel of them.
  * ws: device memory of tps_attn_q8_workspace_size(cap, N, H, d) bytes (0 when no key
  * split is chosen), 16-byte aligned, no initialisation: a dense call whose grid would
  * leave the GPU partly idle (few active rows, or a mostly empty last wave) runs as

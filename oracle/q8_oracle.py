@@ -94,7 +94,7 @@ def q8_attn_bound(q, k, v, vs, idx, scale: float, blockmask=None, floor=None):
     """(tolerance of o [A, H, d], tolerance of lse [A, H]) for float64 k, v [N, H, d] and V's scales vs [nb, H].
 
     With E the mean over the softmax weights p, and e the relative error of an unrounded probability:
-      e    <= scale * (2^-17 max|q| sum|k| + 2 d 2^-23 sum|q||k|)   (q's two 8-bit parts: at most 2^-18 of the
+      e    <= scale * (2^-17 max|q| sum|k| + 2 d 2^-23 sum|q||k|)   (q's two 8-bit parts: at most 2^-17 of the
               row's largest where they are not exact; products summed in fp32, 2 d terms, truncated sums)
               + 2^-22 (|x| + 4)                                       (the fp32 exponent, exp2, reciprocals),
       o:   (2^-11 + 2 e) E|v| + N 2^-25 448 max vs + 2^-8 |o|         (f16 probabilities, normal and below

@@ -88,6 +88,21 @@ def test_kv_sync_q8_oracle_scales_grow_and_do_not_drift():
     assert (s4[0] < s3[0]).all()                                     # ... until the whole block is fresh
 
 
+def test_two_e4m3_parts_hold_a_bf16_row():
+    """q = 2^e (hi + lo): exact down to 2^-9 of the row's largest channel, within 2^-17 of the largest below that; and
+    not 2^-10 and 2^-18 (largest 225, channel 225 * 2^-10)."""
+    mant = (128 + np.arange(128)) / 128.0
+    values = np.concatenate([mant * 2.0 ** e for e in range(-30, 9)])
+    values = values[values <= 448]
+    hi = Q.e4m3_round(values)
+    miss = np.abs(hi + Q.e4m3_round(values - hi) - values)
+    least, most = 224.0 * (1 + 2.0 ** -7), 448.0                     # the scaled largest lies there
+    assert not miss[values >= 2.0 ** -9 * least].any()
+    assert miss.max() <= 2.0 ** -17 * least
+    at = np.flatnonzero(values == 225 * 2.0 ** -10)[0]
+    assert values[at] < 0.25 and miss[at] > 2.0 ** -18 * 225 and Q.q8_scale(225.0) == 1.0 and Q.q8_scale(most) == 1.0
+
+
 # ---- the host-built table --------------------------------------------------------------------------------
 @pytest.mark.parametrize("d,grid,origin,base", [(64, (4, 8, 8), (0, 0, 0), 10000.0), (128, (3, 5, 7), (9, -2, 1000), 500.0)])
 def test_rope_table(d, grid, origin, base):

@@ -11,8 +11,8 @@
 // Nothing of the cache is dequantised to the scaled value:
 // - Q K^T runs as e4m3 MMAs on the codes. A bf16 value has 8 significant bits and an
 //   e4m3 value 4, so q = 2^e (hi + lo) with hi = e4m3(q / 2^e), lo = e4m3(rest) and one
-//   power of two per row with amax(q) <= 448 * 2^e: exact for channels down to 2^-10 of
-//   the row's largest, and within 2^-18 of the largest below that. Two e4m3 MMAs cost what
+//   power of two per row with amax(q) <= 448 * 2^e: exact for channels down to 2^-9 of
+//   the row's largest, and within 2^-17 of the largest below that. Two e4m3 MMAs cost what
 //   one bf16 MMA costs, K stays 8 bits wide in shared memory, and no key is converted.
 // - ks_b enters as the factor of the exponent's FMA. vs_b enters as log2(vs_b) in its
 //   addend, so that P' = 2^(x + log2 vs_b - m) multiplies the codes of V directly; the row
