@@ -874,3 +874,63 @@ def test_attn_q8_takes_its_scale_as_pruned_attn_does():
         tps.pruned_attn(q, kv, kv, *idx, scale)
         assert torch.equal(tps.pruned_attn_q8(q, *cache, *idx, scale), want)
     tps.tps_check()
+
+
+def test_attn_q8_the_tail_plan_is_the_one_that_is_tested():
+    """The shape of test_attn_q8_full_waves_then_a_split_tail splits its last row tiles alone: a plan that split all
+    rows would need room for two parts of each."""
+    N, A, H, d = 2100, 2005, 24, 64
+    need = tps.attn_q8_workspace(A, N, H, d).numel()
+    assert 0 < need < 2 * A * H * (d + 1) * 4
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_attn_q8_nan_scales_of_blocks_that_no_query_keeps(d):
+    N, H, nb = 900, 2, 8
+    cache, q, idx = _attn_case(N, 500, H, d, 77)
+    bm = np.ones((nb, nb), np.uint8)
+    bm[:, [0, 3, 7]] = 0                                             # the first, one between, the last (part of a tile)
+    clean = _run_attn(cache, q, idx, 0.125, bm=bm)
+    _check_attn(*clean, cache, q, idx, 0.125, bm)
+    dev = list(_to_dev(cache))
+    for b in (0, 3, 7):
+        for codes, sc in ((dev[0], dev[2]), (dev[1], dev[3])):
+            codes[b * 128:(b + 1) * 128] = 0x7F
+            sc[b] = float("nan")
+    for got, want in zip(_run_attn(cache, q, idx, 0.125, bm=bm, dev=dev), clean):
+        assert np.array_equal(got, want)
+
+
+@pytest.mark.parametrize("A,masked", [(40, False), (130, False), (130, True)])
+def test_attn_q8_offsets_beyond_32_bits_on_the_tensor_cores(A, masked):
+    """A cache of more than 2^32 code bytes through the tensor maps and the converters, dense (one set, two sets) and
+    with a mask that keeps the first and the last key blocks."""
+    H, d, scale = 128, 128, 0.5
+    N = (1 << 18) + 200
+    nb = (N + 127) // 128
+    kc, vc, ks, vs = tps.cache_q8(N, H, d)
+    idx = np.concatenate([np.arange(64), np.arange(N - 200, N)]).astype(np.int32)
+    k, v, q = (synth.gaussian_bf16((len(idx), H, d), 90 + i) for i in range(3))
+    tps.kv_sync_q8(kc, vc, ks, vs, k.to(DEV), v.to(DEV), *_dev(idx))
+    last = slice(len(idx) - A, len(idx))
+    bm = None
+    if masked:
+        bm = np.zeros((nb, nb), np.uint8)
+        bm[:, [0, nb - 2, nb - 1]] = 1
+    o, lse = _run_attn(None, q[last], idx[last], scale, bm=bm, dev=(kc, vc, ks, vs))
+    rows = torch.from_numpy(idx).long().to(DEV)
+    for h in (0, 127):
+        full = []
+        for codes, sc, x in ((kc, ks, k), (vc, vs, v)):
+            per = sc[rows // 128, h].cpu().double().numpy()[:, None]
+            got = Q.e4m3_decode(codes.view(torch.uint8)[rows, h].cpu().numpy()) * per
+            x = O.f64(x[:, h])
+            assert np.all(np.abs(got - x) <= 2.0 ** -4 * np.abs(x) + 2.0 ** -10 * per)
+            at = np.zeros((N, 1, d))
+            at[idx, 0] = got
+            full.append(at)
+        qh, v_scale = q[last][:, h:h + 1], vs[:, h:h + 1].cpu().double().numpy()
+        ref, rlse = O.pruned_attn(qh, *full, idx[last], scale, blockmask=bm)
+        ot, lt = Q.q8_attn_bound(qh, *full, v_scale, idx[last], scale, bm, floor=2.0 ** -33)
+        assert np.all(np.abs(o[:, h:h + 1] - ref) <= ot)
+        assert np.all(np.abs(lse[:, h:h + 1] - rlse) <= lt)
