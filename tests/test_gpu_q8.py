@@ -934,3 +934,20 @@ def test_attn_q8_offsets_beyond_32_bits_on_the_tensor_cores(A, masked):
         ot, lt = Q.q8_attn_bound(qh, *full, v_scale, idx[last], scale, bm, floor=2.0 ** -33)
         assert np.all(np.abs(o[:, h:h + 1] - ref) <= ot)
         assert np.all(np.abs(lse[:, h:h + 1] - rlse) <= lt)
+
+
+@pytest.mark.parametrize("old", [1e-40, 2.0 ** -127, 2.0 ** -126, 3e38])
+def test_kv_sync_q8_zero_rows_under_an_old_scale_at_the_ends_of_fp32(old):
+    """Zero values are codes of zero whatever positive scale the block has (its reciprocal may be beyond fp32)."""
+    N, H, d = 200, 2, 64
+    cache = _cache(N, H, d, 12)
+    dev = _to_dev(cache)
+    dev[2][0], dev[3][0] = old, old
+    idx = _idx(128, 30, 4)
+    zero = torch.zeros((30, H, d), dtype=torch.bfloat16)
+    tps.kv_sync_q8(*dev, zero.to(DEV), zero.to(DEV), *_dev(idx))
+    tps.tps_check()
+    for i in range(2):
+        vals, sc = cache[i][0], cache[i][1].copy()
+        sc[0] = float(np.float32(old))
+        _check_codes(dev[i], dev[2 + i], *Q.kv_sync_q8(vals, sc, O.f64(zero), idx))

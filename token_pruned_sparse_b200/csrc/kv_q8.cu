@@ -80,7 +80,8 @@ __device__ __forceinline__ uint2 codes_of(const float (&v)[8], float inv) {
   return make_uint2(pack_e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
                     pack_e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
 }
-__device__ __forceinline__ float factor_of(float scale) { return scale > 0.f ? 1.f / scale : 1.f; }
+// (finite: below 2^-128 the reciprocal is not, and 0 times it would be NaN)
+__device__ __forceinline__ float factor_of(float scale) { return scale > 0.f ? fminf(1.f / scale, 3e38f) : 1.f; }
 
 template <int D, bool kTurn>
 __device__ __forceinline__ void sync_block(const SyncQ8& p, int tensor) {
