@@ -21,8 +21,8 @@
 // - P' V needs V as wide as P: four converter warps turn the codes into f16 (exact, e4m3 is
 //   a subset of f16) on the way from global to the swizzled shared tile. P' is f16: 11
 //   bits against bf16's 8 make its rounding (2^-11 per probability) vanish beside the
-//   output's. The reference m is 2^8 below the running maximum of x + log2 vs_b (attn_q8.cuh),
-//   and P' <= 2^15 always (kSumLimit); what underflows is below 2^-33 of the largest P'.
+//   output's. The reference m is up to 2^8 below the running maximum of x + log2 vs_b, the more the
+//   longer the range (attn_q8.cuh), so that what underflows is below 2^-13 of the row; P' <= 2^15 always (kSumLimit).
 //
 // Two layouts of a CTA's two 128-row MMA tiles t = 0, 1 (template kOneSet):
 // - false: 256 compacted rows of one head; both tiles consume every K/V tile.
@@ -595,7 +595,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
           // a tile's first half has a key below N, so the first maximum is finite (or S is NaN, and so is
           // the row); m stays -inf until a key has a value
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-          const float m_new = fmaxf(m_run, top + (lv - kRaise));
+          const float m_new = fmaxf(m_run, top + (lv - raise_of(ntiles)));
           const float s_new = fmaxf(s_run, top);
           const float beta = fast_exp2(s_run - s_new);
           l_run *= beta;
