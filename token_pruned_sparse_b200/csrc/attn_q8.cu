@@ -127,12 +127,6 @@ __device__ __forceinline__ void barrier_softmax() {
   asm volatile("barrier.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
 }
 
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // P' = 2^(S * c - base) of 32 columns as f16 pairs; the unrounded P' are added to acc.
 __device__ __forceinline__ void exp_cols_f16(const uint32_t (&sr)[32], uint64_t c2, uint64_t nb2, uint32_t* pk,
                                              uint64_t (&acc)[2]) {
@@ -389,8 +383,9 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     // ================================ MMA issuer =======================================
     // One thread issues the MMAs of both tiles, in turns, or (one set) each tile has its own. The tensor
     // pipe queues 8 MMAs, about 400 clocks of work, and a commit, a wait that finds its barrier ready and a
-    // tcgen05 fence cost the issuer 50-200 clocks each, so a single one leaves the pipe waiting: with two,
-    // one token over the HSA cache took 154 us instead of 179. With shared key tiles two issuers lose: the
+    // tcgen05 fence cost the issuer 50-200 clocks each, so a single one leaves the pipe waiting: two took 154 us
+    // instead of 179 for one set of rows (a single one) over 118,800 keys, 24 heads, before such calls got a kernel
+    // of their own. With shared key tiles two issuers lose: the
     // tiles fall into step and both softmaxes wait for MMAs at once (middle video 656 us instead of 622).
     // Descriptors are a base plus a constant in the 14-bit address field (shared memory ends
     // below 2^18 bytes: no carry).
@@ -776,20 +771,6 @@ int make_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, int64_t N, int
   return TPS_OK;
 }
 
-template <auto kKernel>
-int smem_attribute(int bytes) {
-  static std::atomic<bool> done[64];   // one set per kernel
-  int dev = 0;
-  cudaGetDevice(&dev);
-  const bool cached = dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire);
-  if (!cached) {
-    cudaError_t e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return cuda_status(e, "pruned_attn_q8: smem attribute");
-    if (dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
-  }
-  return TPS_OK;
-}
-
 // How a call runs. A unit of work is one row tile (256 rows, or one set of 128) of one head; U units on P SMs
 // take ceil(U / P) unit times. Two ways out of a mostly empty last wave: all units split S ways along the
 // keys, or the units of the full waves whole and the remaining tiles split S_t ways in a second launch.
@@ -923,7 +904,7 @@ int launch_merge(const Q8Args& prm, cudaStream_t st) {
 template <int D, bool kOneSet>
 int launch(const CUtensorMap& mk, const CUtensorMap& mv, const Q8Args& prm, int64_t tiles, cudaStream_t st) {
   constexpr int kSmem = Layout<D, kOneSet>::kAlloc;
-  if (int e = smem_attribute<attn_q8_kernel<D, kOneSet>>(kSmem)) return e;
+  if (int e = smem_attribute<attn_q8_kernel<D, kOneSet>>(kSmem, "pruned_attn_q8")) return e;
   const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(prm.a.H), static_cast<unsigned>(prm.nsplit));
   attn_q8_kernel<D, kOneSet><<<grid, kThreads, kSmem, st>>>(mk, mv, prm);
   return launch_status("pruned_attn_q8");

@@ -1437,22 +1437,6 @@ int make_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, int64_t rows, 
   return TPS_OK;
 }
 
-// Sets the kernel's dynamic shared-memory limit once per device (setting it
-// twice is harmless; devices numbered 64 and above set it on every launch).
-template <auto kKernel>
-int smem_attribute(int bytes) {
-  static std::atomic<bool> done[64];   // one set per kernel
-  int dev = 0;
-  cudaGetDevice(&dev);
-  const bool cached = dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire);
-  if (!cached) {
-    cudaError_t e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return cuda_status(e, "pruned_attn: smem attribute");
-    if (dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
-  }
-  return TPS_OK;
-}
-
 // Dense: ceil(cap/256) x H x nsplit CTAs of two 128-row tiles of compacted rows.
 // Masked (block mode): ceil(nb/2) x H CTAs, CTA x holding the active rows of
 // query blocks 2x and 2x+1, each tile with its own key list; with d = 128 the
@@ -1477,18 +1461,18 @@ int launch(const AttnArgs& a, cudaStream_t st, int nsplit = 1, float* o_part = n
       CUtensorMap mq64;
       if (int e = make_map(enc, &mq64, a.q, a.cap, a.H, a.d, blkt::kUR)) return e;
       constexpr int kSmem = blkt::LayoutT::kAlloc;
-      if (int e = smem_attribute<attn_blkt_kernel>(kSmem)) return e;
+      if (int e = smem_attribute<attn_blkt_kernel>(kSmem, "pruned_attn")) return e;
       dim3 grid(static_cast<unsigned int>((a.nb + kQT - 1) / kQT), static_cast<unsigned int>(a.H), kBM / blkt::kUR);
       attn_blkt_kernel<<<grid, blkt::kThreadsT, kSmem, st>>>(mq64, mk, mv, prm);
     } else {
       constexpr int kSmem = Layout<D, kQT>::kAlloc;
-      if (int e = smem_attribute<attn_blk_kernel<D>>(kSmem)) return e;
+      if (int e = smem_attribute<attn_blk_kernel<D>>(kSmem, "pruned_attn")) return e;
       dim3 grid(static_cast<unsigned int>((a.nb + kQT - 1) / kQT), static_cast<unsigned int>(a.H), 1u);
       attn_blk_kernel<D><<<grid, kThreads, kSmem, st>>>(mq, mk, mv, prm);
     }
   } else {
     constexpr int kSmem = Layout<D, 1>::kAlloc;
-    if (int e = smem_attribute<attn_tc_kernel<D, false>>(kSmem)) return e;
+    if (int e = smem_attribute<attn_tc_kernel<D, false>>(kSmem, "pruned_attn")) return e;
     if (ntiles < 0) ntiles = (a.cap + kQT * kBM - 1) / (kQT * kBM);
     dim3 grid(static_cast<unsigned int>(ntiles), static_cast<unsigned int>(a.H), static_cast<unsigned int>(nsplit));
     attn_tc_kernel<D, false><<<grid, kThreads, kSmem, st>>>(mq, mk, mv, prm);
@@ -1510,7 +1494,7 @@ int cluster_slots(int S) {
     const int v = cache[dev][S].load(std::memory_order_acquire);
     if (v > 0) return v - 1;
   }
-  if (smem_attribute<attn_tc_kernel<D, true>>(Layout<D, 1>::kAlloc)) return 0;
+  if (smem_attribute<attn_tc_kernel<D, true>>(Layout<D, 1>::kAlloc, "pruned_attn")) return 0;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(1, 1, static_cast<unsigned int>(S));
   cfg.blockDim = dim3(kThreads, 1, 1);
@@ -1605,7 +1589,7 @@ int launch_cluster(const AttnArgs& a, cudaStream_t st, int S, int64_t tile0 = 0,
   if (int e = make_map(enc, &mq, a.q, a.cap, a.H, a.d)) return e;
   if (int e = make_map(enc, &mk, a.k, a.N, a.H, a.d)) return e;
   if (int e = make_map(enc, &mv, a.v, a.N, a.H, a.d)) return e;
-  if (int e = smem_attribute<attn_tc_kernel<D, true>>(Layout<D, 1>::kAlloc)) return e;
+  if (int e = smem_attribute<attn_tc_kernel<D, true>>(Layout<D, 1>::kAlloc, "pruned_attn")) return e;
   TcParams prm{a, a.scale * kLog2e, status, S, nullptr, nullptr, S, static_cast<int>(tile0)};
   if (ntiles < 0) ntiles = (a.cap + kQT * kBM - 1) / (kQT * kBM);
   cudaLaunchConfig_t cfg{};

@@ -18,6 +18,12 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
 __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
   return pack_e4m3x2(a, b) | (pack_e4m3x2(c, d) << 16);
 }
+// Two fp32 values -> packed f16x2 (lo in bits 0-15), round to nearest even.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 // Two e4m3 codes (bits 0-15 of w) -> packed f16x2; exact (e4m3 is a subset of f16).
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
   uint32_t r;

@@ -26,6 +26,22 @@ unsigned int* device_status(int* err);
 // Number of SMs of the current device (cached per device).
 int sm_count();
 
+// Sets the kernel's dynamic shared-memory limit once per device (setting it
+// twice is harmless; devices numbered 64 and above set it on every launch).
+template <auto kKernel>
+int smem_attribute(int bytes, const char* who) {
+  static std::atomic<bool> done[64];   // one set per kernel
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const bool cached = dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire);
+  if (!cached) {
+    cudaError_t e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return cuda_status(e, who);
+    if (dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
+  }
+  return TPS_OK;
+}
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // ---- device-side helpers -------------------------------------------------------
