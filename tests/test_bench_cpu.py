@@ -55,3 +55,9 @@ def test_other_ranks_exit_without_work():
     r = _run(["--impl", "reference", "--steps", "1", "--warmup", "3"], RANK="1", WORLD_SIZE="2", LOCAL_RANK="1")
     assert r.returncode == 0, r.stderr[-2000:]
     assert r.stdout.strip() == ""
+
+
+@pytest.mark.parametrize("record", ["pruned_attn_hsa.json", "pruned_attn_mid.json"])
+def test_traffic_records_are_of_the_present_attention_sources(record):
+    """The bench line reports DRAM traffic only from a record taken on the sources as they are."""
+    assert bench.recorded_traffic(record) is not None
