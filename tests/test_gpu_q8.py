@@ -951,3 +951,88 @@ def test_kv_sync_q8_zero_rows_under_an_old_scale_at_the_ends_of_fp32(old):
         vals, sc = cache[i][0], cache[i][1].copy()
         sc[0] = float(np.float32(old))
         _check_codes(dev[i], dev[2 + i], *Q.kv_sync_q8(vals, sc, O.f64(zero), idx))
+
+
+@pytest.mark.parametrize("N,A,H,d,masked", [(700, 5, 2, 64, False), (700, 60, 2, 128, False), (700, 300, 2, 64, False),
+                                            (2100, 2000, 24, 64, False), (700, 300, 2, 128, True), (300, 40, 256, 128, False),
+                                            (300, 140, 256, 128, True)])
+def test_attn_q8_in_place_a_smaller_capacity_and_a_mask_of_bools(N, A, H, d, masked):
+    """o_act may be q_act; with cap given, rows behind it stay whatever the count says; a mask may be bool."""
+    cache, q, idx = _attn_case(N, A, H, d, 19)
+    nb = (N + 127) // 128
+    bm = (np.random.default_rng(2).random((nb, nb)) < 0.6) if masked else None
+    scale = 1.0 / math.sqrt(d)
+    dev = _to_dev(cache)
+    want, lse = _run_attn(cache, q, idx, scale, bm=None if bm is None else bm.astype(np.uint8), dev=dev)
+    if H < 100:
+        _check_attn(want, lse, cache, q, idx, scale, bm)
+    else:                                                            # a few of many heads
+        some = [0, 100, H - 1]
+        part = [(v[:, some], s[:, some]) for v, s in cache]
+        _check_attn(want[:, some], lse[:, some], part, q[:, some], idx, scale, bm)
+    mask = None if bm is None else torch.from_numpy(bm).to(DEV)
+    di, dc = _dev(idx)
+    o = q.to(DEV)
+    tps.pruned_attn_q8(o, *dev, di, dc, scale, blockmask=mask, o_act=o)
+    assert np.array_equal(O.f64(o.cpu()), want)
+    cap = A - A // 3
+    o = torch.full((A, H, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    tps.pruned_attn_q8(q.to(DEV), *dev, di, dc, scale, blockmask=mask, o_act=o, cap=cap)
+    tps.tps_check()
+    assert bool((o[cap:] == 7.0).all())
+    tol, _ = Q.q8_attn_bound(q[:cap, :1], *(v[:, :1] for v in _values(cache)), cache[1][1][:, :1], idx[:cap], scale, bm)
+    assert np.all(np.abs(O.f64(o[:cap, :1].cpu()) - want[:cap, :1]) <= 2 * tol)      # (another plan, other roundings)
+
+
+def test_attn_q8_a_mask_of_the_largest_size():
+    """4,096 key blocks: a query block that keeps all of them, and one that keeps the last alone."""
+    N, H, d, A = 4096 * 128, 1, 64, 40
+    kc, vc, ks, vs = tps.cache_q8(N, H, d)
+    rows = np.unique(np.concatenate([np.random.default_rng(0).integers(0, N, 400), [0, N - 1]])).astype(np.int32)
+    k, v = (synth.gaussian_bf16((len(rows), H, d), 95 + i) for i in range(2))
+    tps.kv_sync_q8(kc, vc, ks, vs, k.to(DEV), v.to(DEV), *_dev(rows))
+    idx = np.concatenate([np.arange(5, 25), np.arange(N - 60, N - 40)]).astype(np.int32)
+    bm = np.zeros((4096, 4096), np.uint8)
+    bm[0], bm[4095, 4095] = 1, 1
+    q = synth.gaussian_bf16((A, H, d), 99)
+    o, lse = _run_attn(None, q, idx, 1.0, bm=bm, dev=(kc, vc, ks, vs))
+    cache = [(Q.e4m3_decode(c.cpu().view(torch.uint8).numpy()), s.cpu().double().numpy()) for c, s in ((kc, ks), (vc, vs))]
+    _check_attn(o, lse, cache, q, idx, 1.0, bm)
+
+
+def test_kv_sync_q8_all_heads_of_a_large_cache_in_one_block():
+    """256 heads and enough blocks that a thread block takes all heads of its tokens."""
+    N, H, d = 60000, 256, 64
+    kc, vc, ks, vs = tps.cache_q8(N, H, d)
+    idx = np.concatenate([np.arange(256, 384), [5, 1000, 1001, 59999]]).astype(np.int32)
+    idx.sort()
+    k, v = (synth.gaussian_bf16((len(idx), H, d), 85 + i) for i in range(2))
+    for scale in (1.0, 4.0):                                         # the second time every scale grows
+        tps.kv_sync_q8(kc, vc, ks, vs, (scale * k.float()).bfloat16().to(DEV), (scale * v.float()).bfloat16().to(DEV), *_dev(idx))
+    tps.tps_check()
+    for codes, sc, x in ((kc, ks, k), (vc, vs, v)):
+        touched = np.unique(idx // 128)
+        assert int((sc != 0).any(1).sum()) == len(touched)
+        for b in touched:
+            mine = idx // 128 == b
+            n = min(128, N - b * 128)
+            ref = Q.kv_sync_q8(np.zeros((n, H, d)), np.zeros((1, H)), O.f64(x)[mine] * 4.0, idx[mine] - b * 128)
+            _check_codes(codes[b * 128:b * 128 + n], sc[b:b + 1], *ref)
+
+
+@pytest.mark.parametrize("dims", [(64, 0, 0), (0, 64, 0), (0, 0, 64), (0, 30, 34), (2, 60, 2)])
+def test_rope_groups_of_any_width(dims):
+    grid, H, d = (3, 5, 7), 2, 64
+    table = tps.rope_table(dims, grid)
+    x = synth.gaussian_bf16((40, H, d), 3)
+    idx = _idx(105, 40, 6)
+    got = tps.rope_rows(x.to(DEV), *_dev(idx), table, dims, grid)
+    ref = O.rope_rows(x, idx, dims, grid)
+    assert np.all(np.abs(O.f64(got.cpu()) - ref) <= _rope_bound(ref, x))
+    cache = tps.cache_q8(105, H, d)
+    tps.kv_sync_q8(*cache, x.to(DEV), x.to(DEV), *_dev(idx), rope=(table, dims, grid))
+    tps.tps_check()
+    zero = (np.zeros((105, H, d)), np.zeros((1, H)))
+    a = np.abs(O.f64(x))
+    slack = 2.0 ** -22 * np.repeat(a[..., 0::2] + a[..., 1::2], 2, axis=-1)
+    _check_codes(cache[0], cache[2], *Q.kv_sync_q8(*zero, ref, idx), ref, idx, slack)
