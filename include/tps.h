@@ -417,9 +417,9 @@ TPS_API int pruned_attn_mma(const tps_bf16* q_act, const tps_bf16* k, const tps_
  * with the blockmask, lse and empty-row rules of pruned_attn. With a mask, idx must be
  * ascending and unique; rows whose entry lies outside [0, N), and a block's rows beyond
  * 128, are left as they were and flagged (TPS_ERR_BOUNDS at tps_check). Without a mask idx
- * is not read. Rows j >= min(*count, cap) of o_act and lse are left as they were. Scales must be finite
- * and >= 0 (a scale of 0 stands for values of 0), the non-zero v_scale within
- * [2^-100, 2^100], in any ratio to each other. The codes are used as they are: Q enters
+ * is not read. Rows j >= min(*count, cap) of o_act and lse are left as they were; o_act may
+ * be q_act. Scales must be finite and >= 0 (a scale of 0 stands for values
+ * of 0), the non-zero v_scale within [2^-100, 2^100], in any ratio to each other. The codes are used as they are: Q enters
  * the e4m3 products as two e4m3 parts (exact for channels down to 2^-9 of a row's
  * largest, within 2^-17 of the largest below that; a row whose largest is below 2^-117
  * keeps fewer bits), the probabilities and V's codes meet in f16 (what that drops of a

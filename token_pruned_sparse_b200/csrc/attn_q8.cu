@@ -44,9 +44,11 @@
 //   - one elected thread and precomputed descriptors (22 clocks per MMA): 760 us;
 //   - S through the registers 32 columns at a time instead of 128 (no spills): 680 us;
 //   - S in two halves per tile, so that MMAs run under the exponentials: 620 us;
-//   - registers moved to the roles that spilled, Q's parts made by rows: 616 us = 1,230 TFLOP/s.
-// Back to back the GPU's power limit holds it to 700-715 us (1.70 GHz): the bf16 kernel takes 675 us there
-// and reads twice the cache.
+//   - registers moved to the roles that spilled, Q's parts made by rows: 616 us;
+//   - the sum against a reference of its own, with a factor per tile instead of a division: 608 us = 1,250 TFLOP/s.
+// Back to back the GPU's power limit holds it to 690-715 us (1.70 GHz), and the bf16 kernel, which reads twice the
+// cache, to 675-715. With d = 64 the exponentials bound it: 552 us for the same rows and keys, of which exp2 alone
+// takes 318 at 1.965 GHz (unit 66% active, tensor pipe 32%); the bf16 kernel takes 543-553.
 #include "attn_q8.cuh"
 #include "q8.cuh"
 #include "tc_ptx.cuh"

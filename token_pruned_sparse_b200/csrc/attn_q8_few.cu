@@ -6,11 +6,11 @@
 // 2 H d bytes per key and 4 rows d FLOP, 111 us for one token over the HSA cache (0.73
 // GB) at the measured copy rate. The tcgen05 kernel pays a 128-row product for it: 156 us
 // in a single call, 180 us back to back, where its MMAs draw the clock down. This
-// one takes 136 us with the merge in a graph (5.4 TB/s) and 142-147 us as a call; loads of the same
-// addresses without any arithmetic take 120 us. The 12 warps per SM wait for memory half of the time. Slower:
-// a ring of 4 steps through shared memory instead of the registers (156-165 us), adjacent heads side by side in
-// a CTA (152-160), a prefetch of lines into L2 (145-177), e4m3 products for S (162, more registers), two chains
-// of products for S instead of four (146). A warp works on its own, without shared memory, barriers or TMEM:
+// one takes 126 us with the merge in a graph (5.8 TB/s) and 133-138 us as a call; loads of the same
+// addresses without any arithmetic take 120 us. The 12 warps per SM wait for memory half of the time. Slower (than
+// an earlier 141 us a call, which spilled 12 bytes at D = 128): a ring of 4 steps through shared memory instead of
+// the registers (156-165 us), adjacent heads side by side in a CTA (152-160), a prefetch of lines into L2 (145-177),
+// e4m3 products for S (162, more registers), two chains of products for S instead of four (146). A warp works on its own, without shared memory, barriers or TMEM:
 // - It owns whole blocks of 128 keys (one scale each) and goes over them 16 keys at
 //   a time, the next 16 keys' codes (4 KB a warp) in flight meanwhile.
 // - S = Q K^T and O^T = V^T P'^T are warp-level f16 products of 16 x 8 x 16; the codes

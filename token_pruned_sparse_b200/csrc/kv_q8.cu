@@ -20,9 +20,15 @@
 // rows once: a warp takes 512 contiguous bytes of each of a part of the rows, 8 loads in
 // flight, turns them, keeps the maximum, and writes the codes against the OLD scale, which
 // is the new one as long as the block got no louder. Heads whose scale does change are
-// read again (from L2) and encoded again. Measured at the HSA size (0.73 GB): CTA-wide passes
-// of 128 (row, head) slots with the block's values held in registers 466 us, a warp holding
-// its head's rows 210-220 us, this 155 us (3 CTAs per SM of 80 registers instead of 2 of 116: 173).
+// read again (from L2) and encoded again. Measured at the HSA size (39,600 rows, 0.73 GB, floor 111
+// us) with scales that stay: CTA-wide passes of 128 (row, head) slots with the block's values held in
+// registers 466 us, a warp holding its head's rows 210-220 us, this 151-155 us (3 CTAs per SM of 80
+// registers instead of 2 of 116: 173), 183 as a single call after a flush of L2.
+// The price: where scales change the second pass has one load in flight per warp and stale rows go 8
+// bytes a lane. Single calls after a flush: the same update four times as loud, so that every scale
+// grows (1.70 GB with the stale rows, floor 260 us), 900 us; the first fill of all 118,800 rows (2.19
+// GB, 334 us) 1,190 us; five new frames of 1,560 tokens, 12 heads (72 MB, 11 us) 27 us where no scale
+// changes, 45 us where 7% of the keys' do.
 #include <climits>
 
 #include "q8.cuh"
