@@ -424,7 +424,7 @@ TPS_API int pruned_attn_mma(const tps_bf16* q_act, const tps_bf16* k, const tps_
  * largest, within 2^-17 of the largest below that; a row whose largest is below 2^-117
  * keeps fewer bits), the probabilities and V's codes meet in f16 (what that drops of a
  * range of n keys is below 2^-13 of its largest term up to 2^20 keys, n 2^-33 of it
- * beyond), sums are fp32. Key blocks
+ * beyond), sums are fp32; outputs below 2^-100 keep fewer bits or become 0. Key blocks
  * that a mask leaves out are not read, nor are their scales. A NaN code of K in an attended
  * block makes the rows that attend it NaN, one of V its channel of them.
  * ws: device memory of tps_attn_q8_workspace_size(cap, N, H, d) bytes (0 when no key

@@ -775,6 +775,8 @@ SPREADS = {
     "a little weight on empty blocks": [(0, 0)] * 3 + [(None, -12)] * 9,
     "half of the weight on a block 2^70 below": [(-40, 0), (30, 0)] * 6,
     "steps of 2^50": [(-100 + 50 * (i % 5), -10 * (i % 3)) for i in range(12)],
+    "weights of 2^-150 on values that are 2^167 larger": [(-72, 150)] * 6 + [(95, 0)] * 6,
+    "the same, larger values first": [(95, 0)] * 6 + [(-72, 150)] * 6,
     "all empty": [(None, 3 * (i % 2)) for i in range(12)],
     "all small": [(-100, i) for i in range(12)],
     "all large": [(100, -i) for i in range(12)],

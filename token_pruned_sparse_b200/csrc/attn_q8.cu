@@ -76,7 +76,7 @@ static_assert(8 * kSoftmaxRegs + 4 * kConvRegs + 4 * kProducerRegs <= 16 * kLaun
 constexpr int kTmemCols = 512;
 constexpr int kListMax = 4096;
 constexpr float kSumLimit = 32768.f;   // largest sum of a row's half tile kept without a new reference: P' stays finite in f16
-static_assert(64 * 256.f <= kSumLimit, "a half tile against its own reference: 64 P' of 2^kRaise");
+static_assert(64.f * (1 << kRaise) <= kSumLimit, "a half tile against its own reference: 64 P' of 2^kRaise");
 static_assert(kBN == kScaleBlock, "a key tile has one scale");
 
 template <int D, bool kOneSet>
@@ -833,7 +833,8 @@ size_t ws_bytes_of(const Plan& plan, int64_t cap, int H, int d) {
 
 // The S-way merge of the partials: o = sum_s w_s o_s / sum_s w_s with w_s = exp(lse_s - max). Latency is all it
 // costs, so a thread (4 channels of a row) loads values and statistics of 8 parts at a time, guarded rather than
-// in a remainder loop, against a running maximum.
+// in a remainder loop, against a running maximum. A weight enters as its root, twice: below 2^-126 it can still count,
+// where the part's values are as much larger than the others'.
 template <int D>
 __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Q8Args prm) {
   asm volatile("griddepcontrol.wait;" ::: "memory");   // launched ahead of the partials' end
@@ -861,17 +862,17 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Q8Ar
 #pragma unroll
       for (int u = 0; u < kParts; ++u) m = fmaxf(m, l[u]);              // NaN is passed over here, not by w
       ref = m == -INFINITY ? 0.f : m;
-      const float f = expf(was - ref);
-      a = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
-      sum *= f;
+      const float f = expf(0.5f * (was - ref));
+      a = make_float4(a.x * f * f, a.y * f * f, a.z * f * f, a.w * f * f);
+      sum *= f * f;
 #pragma unroll
       for (int u = 0; u < kParts; ++u) {
-        const float w = expf(l[u] - ref);
-        a.x = fmaf(w, x[u].x, a.x);
-        a.y = fmaf(w, x[u].y, a.y);
-        a.z = fmaf(w, x[u].z, a.z);
-        a.w = fmaf(w, x[u].w, a.w);
-        sum += w;
+        const float w = expf(0.5f * (l[u] - ref));
+        a.x = fmaf(w, w * x[u].x, a.x);
+        a.y = fmaf(w, w * x[u].y, a.y);
+        a.z = fmaf(w, w * x[u].z, a.z);
+        a.w = fmaf(w, w * x[u].w, a.w);
+        sum = fmaf(w, w, sum);
       }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
