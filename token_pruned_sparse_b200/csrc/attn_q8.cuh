@@ -30,9 +30,10 @@ constexpr float kScaleMin = 7.8886091e-31f, kScaleMax = 1.2676506e30f;   // 2^-1
 // r = 0, 3% at a million keys). A high r leaves less room for the keys to come: rows meet a new reference sooner.
 // So r grows with the range (raise_of): n 2^-(25 + r) <= 2^-13 up to 2^20 keys, and 2^-33 of them beyond. r = 8
 // everywhere takes 428 us instead of 385 for a masked call of 24 blocks a row, where r = 0 does, and 725 instead of
-// 714 for 6,084 rows over 20,280 keys (r = 3), on one GPU. The few-row kernel's references cost little: kRaise. A key's share of the sum is P' 2^(m - log2 vs - s). Up to kShareMax of that
-// factor a P' that underflows (2^-126) is of a key below 2^-66 of the sum. Beyond it (blocks whose vs is far below
-// others'), and where vs is 0 (values of 0: P' = 0), a second pass of exponentials takes the sum.
+// 714 for 6,084 rows over 20,280 keys (r = 3), on one GPU. The few-row kernel's references cost little: r = kRaise.
+// A key's share of the sum is P' 2^(m - log2 vs - s). Up to kShareMax of that factor a P' that underflows (2^-126) is
+// of a key below 2^-66 of the sum. Beyond it (blocks whose vs is far below others'), and where vs is 0 (values of 0:
+// P' = 0), a second pass of exponentials takes the sum.
 constexpr int kRaise = 8;
 __device__ __forceinline__ float raise_of(int tiles) {   // of 128 keys: ceil(log2(tiles)) - 5, from 0 to kRaise
   const int r = 27 - __clz(tiles - 1);
