@@ -33,7 +33,8 @@ constexpr float kScaleMin = 7.8886091e-31f, kScaleMax = 1.2676506e30f;   // 2^-1
 // 714 for 6,084 rows over 20,280 keys (r = 3), on one GPU. The few-row kernel's references cost little: r = kRaise.
 // A key's share of the sum is P' 2^(m - log2 vs - s). Up to kShareMax of that factor a P' that underflows (2^-126) is
 // of a key below 2^-66 of the sum. Beyond it (blocks whose vs is far below others'), and where vs is 0 (values of 0:
-// P' = 0), a second pass of exponentials takes the sum.
+// P' = 0), a pass of exponentials of its own takes the sum: with a quarter of the blocks empty 6,084 rows over 20,280
+// keys take 748 us instead of 614 (empty tiles on the fast path instead spilled registers, 739 us for every call).
 constexpr int kRaise = 8;
 __device__ __forceinline__ float raise_of(int tiles) {   // of 128 keys: ceil(log2(tiles)) - 5, from 0 to kRaise
   const int r = 27 - __clz(tiles - 1);
